@@ -968,14 +968,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
         // them the tensor cores soon idle (two warps that issue in turn are slower still): what stands between groups
         // is kept short, and the waits of a group are polled together.
         auto wait = [&](int code, auto... polls) {  // every lane polls for itself; the one that issues has seen the phases
-          for (uint32_t n = 0; !(polls() & ...); ++n) {
+          bool ok = true;
+          for (uint32_t n = 0; ok && !(polls() & ...); ++n) {
             if ((n & 255) == 255 && (*abort_flag || n > kTries)) {
               if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) atomicCAS(&g_chunk_error, 0, code);
-              return false;
+              ok = false;
             }
           }
+          // No lane goes on before all have seen the phases: they turn every tile, and a lane that fell two turns behind
+          // the one that issues would wait for a phase that is over.
+          ok = __all_sync(0xFFFFFFFFu, ok);
           tc_after();
-          return true;
+          return ok;
         };
         uint32_t ph = 0;            // phase of what turns once a tile, of the tile whose sums come next
         uint32_t ks = 0, kph = 0;   // stage and phase of the next scores' keys
