@@ -4,10 +4,14 @@
 //
 // With block exponents eK, eV and codes k, v of a visible key j, in f32:
 //   s_j = scale * log2(e) * 2^eK * (q . k_j)
-//   t_j = s_j + eV,  m = max_j t_j,  p_j = 2^(t_j - m)
+//   m = the key whose s_m + eV_m is largest,  p_j = 2^((s_j - s_m) + (eV_j - eV_m))
 //   out = sum_j p_j v_j / sum_j p_j 2^-eV
 // The value scale costs an addition in the exponent and a multiplication per
-// block in the sum instead of one per code.
+// block in the sum instead of one per code. Scores are subtracted from scores
+// before the exponents are added: where scores are so large that their
+// spacing exceeds the exponents (or the constant that the weights are held
+// up by), a sum of the two would be rounded to another weight, one that f16
+// may not hold.
 //
 // Bound by the cache's bytes: an SM receives about 23 bytes a cycle at the
 // measured copy rate. One token of 64 sequences (1 to 8191 keys, 32 / 16
@@ -109,7 +113,7 @@ struct Shape {
   static constexpr int kWarps = kFit < kMost ? kFit : kMost;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kSmem = kWarps * (kStage + kQBytes);
-  static constexpr int kPart = ROWS * D + 2 * ROWS;      // floats of a partial result: sums, maxima, denominators
+  static constexpr int kPart = ROWS * D + 3 * ROWS;      // floats of a partial result: sums, maxima, denominators, maxima's exponents
 };
 
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -144,6 +148,14 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Whether key a (score, value exponent) weighs more than key b; false where there is no a.
+__device__ __forceinline__ bool heavier(float sa, float ea, float sb, float eb) { return (sa - sb) + (ea - eb) > 0.f; }
+// The heavier of the lane's key and that of lane ^ d; both lanes choose alike, the larger score where they weigh the same.
+__device__ __forceinline__ void heavier_of(float& s, float& e, int d) {
+  const float s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d), e2 = __shfl_xor_sync(0xFFFFFFFFu, e, d), more = (s2 - s) + (e2 - e);
+  if (more > 0.f || (more == 0.f && s2 > s)) s = s2, e = e2;
 }
 
 // A sequence's share of the list: row tiles x heads x tiles.
@@ -206,9 +218,9 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
   __shared__ uint32_t s_mates[2 * S::kWarps];      // the pieces of a piece's head, itself included
   __shared__ int s_heads[2 * S::kWarps], s_nheads;  // first piece of each head that has some
   __shared__ __align__(16) float s_max[2 * S::kWarps][ROWS], s_sum[2 * S::kWarps][ROWS], s_weight[2 * S::kWarps][ROWS],
-      s_top[2 * S::kWarps][ROWS], s_inv[2 * S::kWarps][ROWS];
+      s_top[2 * S::kWarps][ROWS], s_inv[2 * S::kWarps][ROWS], s_max_e[2 * S::kWarps][ROWS], s_top_e[2 * S::kWarps][ROWS];
   // of the pieces: maxima, denominators (a head's first piece: the head's), weights in their head; of heads, at the first
-  // piece: maxima, reciprocals of the denominators
+  // piece: maxima, reciprocals of the denominators; value exponents of both maxima
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, t = lane & 3;
   const int seqs = (int)g.b.seqs, group = (int)g.a.group;
@@ -398,8 +410,9 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
 
     // accumulators of rows 8 h + 2 t, + 1 and channels 16 i + g, + 8: [channel][row]
     float o[kOut][H][4];
-    // of row 8 h + g: running maximum, this lane's share of the denominator, scale of the scores, position, first key
-    float m[H], l[H], fq[H];
+    // of row 8 h + g: score and value exponent of the heaviest key so far, this lane's share of the denominator, scale of
+    // the scores, position, first key
+    float m[H], me[H], l[H], fq[H];
     int pos[H], low[H], pos_min = 0, low_max = 0;
 
     // the rows of a (row tile, head): their positions, and the queries as operands
@@ -413,6 +426,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         pos[h] = ok ? start + i : -1;
         low[h] = g.a.window > 0 ? (int)max((int64_t)pos[h] - g.a.window + 1, (int64_t)0) : 0;
         m[h] = -INFINITY;
+        me[h] = 0.f;
         l[h] = 0.f;
         const T* q = static_cast<const T*>(g.a.q) + (int64_t)(sq.first + (ok ? i : 0)) * g.a.q_stride + (int64_t)(out.head * group + row % group) * D;
         // a panel's chunks 2 t and 2 t + 1 of 16 channels are this lane's (64 channels: chunk t)
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
     uint32_t p[H][8];  // weights: token pair j of block t, row 8 h + g
     auto weights = [&](int tok0, int k_e, int v_e, uint32_t blocks, bool clean) {
       const float fk = exp2i(k_e), fe = (float)v_e, fl = exp2i(-v_e);
-      float keep[H], base[H];
+      float keep[H], base[H], up[H];
       bool grew = false;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
@@ -539,7 +553,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
           for (int i = 0; i < 2; ++i) {
             // eight rows: rows 8..15 of the product are the second term
             float& v = sc[j][2 * h + i];
-            v = fmaf(ROWS == 8 ? fmaf(sc[j][2 + i], 0.0625f, v) : v, f, fe);
+            v = (ROWS == 8 ? fmaf(sc[j][2 + i], 0.0625f, v) : v) * f;
           }
         if (!clean) {
 #pragma unroll
@@ -552,14 +566,17 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const float mn = fmaxf(m[h], top);
+        float te = fe;
+        heavier_of(top, te, 1);
+        heavier_of(top, te, 2);
+        const bool more = heavier(top, te, m[h], me[h]);
+        const float mn = more ? top : m[h], en = more ? te : me[h];
         base[h] = mn == -INFINITY ? 0.f : mn;
-        keep[h] = ex2(m[h] - base[h]);
-        grew |= mn != m[h];
+        keep[h] = ex2((m[h] - base[h]) + (me[h] - en));
+        grew |= more;
         m[h] = mn;
-        base[h] -= kPUp;
+        me[h] = en;
+        up[h] = fe - en + kPUp;
       }
       if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
@@ -575,7 +592,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float x = ex2(sc[j][2 * h] - base[h]), y = ex2(sc[j][2 * h + 1] - base[h]);
+          const float x = ex2((sc[j][2 * h] - base[h]) + up[h]), y = ex2((sc[j][2 * h + 1] - base[h]) + up[h]);
           sum += x + y;
           p[h][j] = pack2<__half>(x, y);
         }
@@ -637,7 +654,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const float sum = row_sum(h);
-        if (t == 0) s_max[piece][gr + 8 * h] = m[h], s_sum[piece][gr + 8 * h] = sum;
+        if (t == 0) s_max[piece][gr + 8 * h] = m[h], s_max_e[piece][gr + 8 * h] = me[h], s_sum[piece][gr + 8 * h] = sum;
         float* p = dst + gr * ROWS + 8 * h + 2 * t;
 #pragma unroll
         for (int i = 0; i < kOut; ++i) {
@@ -735,14 +752,19 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
   for (int idx = tid; idx < 2 * S::kWarps * ROWS; idx += S::kThreads) {  // weights of the pieces' rows
     const int i = idx / ROWS, r = idx % ROWS;
     if (!(pieces >> i & 1)) continue;
-    float top = -INFINITY;
-    for (uint32_t k = s_mates[i]; k; k &= k - 1) top = fmaxf(top, s_max[__ffs(k) - 1][r]);
+    float top = -INFINITY, te = 0.f;
+    for (uint32_t k = s_mates[i]; k; k &= k - 1) {
+      const float s = s_max[__ffs(k) - 1][r], e = s_max_e[__ffs(k) - 1][r];
+      if (heavier(s, e, top, te)) top = s, te = e;
+    }
     const float base = top == -INFINITY ? 0.f : top;
-    s_weight[i][r] = ex2(s_max[i][r] - base);
+    auto weight = [&](int j) { return ex2((s_max[j][r] - base) + (s_max_e[j][r] - te)); };
+    s_weight[i][r] = weight(i);
     if (__ffs(s_mates[i]) - 1 != i) continue;
     float sum = 0.f;
-    for (uint32_t k = s_mates[i]; k; k &= k - 1) sum = fmaf(ex2(s_max[__ffs(k) - 1][r] - base), s_sum[__ffs(k) - 1][r], sum);
+    for (uint32_t k = s_mates[i]; k; k &= k - 1) sum = fmaf(weight(__ffs(k) - 1), s_sum[__ffs(k) - 1][r], sum);
     s_top[i][r] = top;
+    s_top_e[i][r] = te;
     s_sum[i][r] = sum;
     s_inv[i][r] = sum == 0.f ? 0.f : 1.f / sum;
   }
@@ -809,6 +831,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
       if (d < 8) {
         part[ROWS * D + r + d] = s_top[i0][r + d];
         part[ROWS * D + ROWS + r + d] = s_sum[i0][r + d];
+        part[ROWS * D + 2 * ROWS + r + d] = s_top_e[i0][r + d];
       }
     }
   }
@@ -837,7 +860,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
     // Weights of the results in shared memory, and after them as many results' sums at a time as there is room for:
     // loads in a loop would each wait for the one before.
     constexpr int kBytes = ROWS * D * 4, kPer = (kItems + S::kThreads - 1) / S::kThreads;
-    const int at = (2 * n * ROWS * 4 + 127) / 128 * 128, room = (S::kSmem - at) / kBytes;
+    const int at = (3 * n * ROWS * 4 + 127) / 128 * 128, room = (S::kSmem - at) / kBytes;
     float* const weight = reinterpret_cast<float*>(smem);
     float4 x[kPer];
 #pragma unroll
@@ -857,16 +880,20 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
           const float* p = part_of(i / ROWS) + ROWS * D + i % ROWS;
           weight[i] = __ldcg(p);
           weight[n * ROWS + i] = __ldcg(p + ROWS);
+          weight[2 * n * ROWS + i] = __ldcg(p + 2 * ROWS);
         }
         __syncthreads();
         for (int r = warp; r < ROWS; r += S::kWarps) {
-          float top = -INFINITY, sum = 0.f;
-          for (int i = lane; i < n; i += 32) top = fmaxf(top, weight[i * ROWS + r]);
+          float top = -INFINITY, te = 0.f, sum = 0.f;
+          for (int i = lane; i < n; i += 32) {
+            const float s = weight[i * ROWS + r], e = weight[(2 * n + i) * ROWS + r];
+            if (heavier(s, e, top, te)) top = s, te = e;
+          }
 #pragma unroll 1
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          for (int o = 16; o; o >>= 1) heavier_of(top, te, o);
           const float base = top == -INFINITY ? 0.f : top;
           for (int i = lane; i < n; i += 32) {
-            const float f = ex2(weight[i * ROWS + r] - base);
+            const float f = ex2((weight[i * ROWS + r] - base) + (weight[(2 * n + i) * ROWS + r] - te));
             weight[i * ROWS + r] = f;
             sum = fmaf(f, weight[(n + i) * ROWS + r], sum);
           }
@@ -920,7 +947,7 @@ cudaError_t launch_shape(AttnArgs g, cudaStream_t st) {
   using S = Shape<T, D, ROWS>;
   constexpr int smem = S::kSmem;
   static_assert(S::kStage >= S::kPart * 4, "a partial result takes a tile's place");
-  static_assert(S::kSmem >= 2 * kKvMaxCtas * ROWS * 4 + ROWS * D * 4, "a join has room for the weights and one result");
+  static_assert(S::kSmem >= 3 * kKvMaxCtas * ROWS * 4 + ROWS * D * 4, "a join has room for the weights and one result");
   auto kern = kv_stream_kernel<T, D, ROWS>;
   int dev = 0, sms = 0;
   static std::atomic<int> ready[kDevices];  // SMs of a device on which the kernel's shared memory is allowed

@@ -1,0 +1,73 @@
+"""Values at the ends of what the cache attention takes: very large and very small scores, queries with channels of
+very different size. Each against the float64 oracle, with a bound that does not grow with the scores."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_oracle as K
+from test_gpu_kv import DT, HALF_ULP, Step, nv  # noqa: F401
+
+# (the oracle's own bound on the results, which grows with the scores, overflows here and is not used)
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:overflow encountered", "ignore:invalid value encountered")]
+
+SIZES = [(64, "bf16"), (64, "f16"), (128, "bf16"), (128, "f16"), (256, "bf16"), (256, "f16")]
+LOG2E = 1.4426950408889634
+
+
+def set_keys(s, values):
+    """Writes key value values[j] into all channels of token j of sequence 0 ([length] or [length, dim])."""
+    places, page = K.key_places(s.dim), s.cache[2].shape[2] * 16
+    for j, v in enumerate(values):
+        pg, inner = s.table[0, j // page], (j % page) // 16
+        for h in range(s.kv_heads):
+            s.cache[0][pg, h, inner, places[j % 16]] = K.encode(np.broadcast_to(v, s.dim) * 2.0 ** (127 - int(s.cache[2][pg, h, inner])))
+    s.load()
+
+
+def absolute_values(s):
+    """The same step over a cache whose values are their magnitudes: its attention is sum w |v|."""
+    return [s.cache[0], s.cache[1] & 0x7F, s.cache[2], s.cache[3]]
+
+
+# Softmax weights are rounded to f16 (2^-12 of each) and the sums to f32, for which 2^-11 leaves room.
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("score", [2.0**12.1, 2.0**20.4, 2.0**24.7, 2.0**26.3, 2.0**27.9, 2.0**30.2])
+@pytest.mark.parametrize("new", [1, 2])
+def test_large_scores_of_equal_keys(nv, dim, dt, score, new):  # noqa: F811
+    """Some keys score the same, all others at least a fourteenth less: the mean of the former's values, whatever the
+    scales of the blocks that they lie in, at any size of the scores (in the exponent of 2)."""
+    s = Step(nv, 50, [new], [3000], 2, 1, dim, 64, dt)
+    length = int(s.lengths[0])
+    s.cache[2][:] = np.where(s.g.integers(0, 2, size=s.cache[2].shape) == 1, 127 - 8, 127 - 7)
+    values = s.g.choice([0.5, -1.0, 0.75, 1.0, 1.625], size=length)
+    values[s.g.choice(length, size=90, replace=False)] = 1.75
+    values[:3] = 1.75
+    set_keys(s, values)
+    q = torch.full((new, 2, dim), 1.37).to(DT[dt])
+    scale = score / (LOG2E * dim * 1.75 * float(q[0, 0, 0]))
+    y, ref, _ = s.attend(q, scale=scale)
+    mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, scale)
+    lim = 2.0**-11 * mean + HALF_ULP[dt] * np.abs(ref) + (2.0**-24 if dt == "f16" else 0.0)
+    err = np.abs(y.double().cpu().numpy() - ref)
+    assert (err <= lim).all(), float((err / lim).max())
+
+
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("score", [2.0**24.2, 2.0**25.6, 2.0**26.9, 2.0**28.5, 2.0**30.1])
+@pytest.mark.parametrize("new", [1, 2])
+def test_large_scores_close_together(nv, dim, dt, score, new):  # noqa: F811
+    """Scores a few units of their last place apart, growing and falling from tile to tile: which key is heaviest is a
+    matter of rounding, but a result lies between the smallest and the largest value."""
+    s = Step(nv, 51, [new], [3000], 2, 1, dim, 64, dt)
+    length = int(s.lengths[0])
+    s.cache[2][:] = 127 - 8
+    values = np.full((length, dim), 1.75)
+    values[:, 0] = s.g.choice([1.0, 1.25, 1.5, 1.75], size=length) * np.where(np.arange(length) // 256 % 2, 1, 0.5)
+    set_keys(s, values)
+    q = torch.full((new, 2, dim), 1.5).to(DT[dt])
+    q[..., 0] = 1.5 * 2.0**-11
+    y, _, _ = s.attend(q, scale=score / (LOG2E * dim * 1.75 * 1.5))
+    _, v, _ = K.dense(s.cache, s.table[0], length)
+    y, most, least = y.double().cpu().numpy(), v.max((0, 1)), v.min((0, 1))
+    slack = (2.0**-11 + HALF_ULP[dt]) * np.abs(v).max((0, 1))
+    assert np.isfinite(y).all() and (y <= most + slack).all() and (y >= least - slack).all()
