@@ -52,6 +52,10 @@ constexpr int kKeys = 128;       // keys of a tile
 constexpr int kPanel = 64;       // tokens of a panel of converted values: rows of 128 bytes
 constexpr float kPUp = 7.0f;     // the weights are held times 2^7
 constexpr float kSlack = 8.0f;   // growth of a maximum that is left to the weights
+// Beyond this a tile's scores are subtracted from one another before the values' exponents are added to them (as the
+// streaming kernel always does): the sum of both, and of what the weights are held up by, would be rounded by more than the
+// weights are to f16. Up to it the three go into the exponential's multiply-add, which takes no instruction more.
+constexpr float kFar = 4096.0f;
 constexpr int kThreads = 512;    // two softmax warpgroups, the converters, copies and products
 // Units (see Walk) of a run at least, for blocks of rows of so many units: shorter runs use more SMs, but the last CTA of
 // a block joins a result of each, which takes it about half as long as a tile. The sum is least at sqrt(units / 2).
@@ -86,7 +90,7 @@ struct Shape {
   static constexpr int kSlots = D == 256 ? 2 : 4;          // panels of each
   static constexpr int kSmem = kQ + kKStages * kK + kSlots * (kRaw + kVal);
   static constexpr uint32_t kPCol = 128, kOCol = 256;      // TMEM: scores from column 0, weights, sums
-  static constexpr int64_t kPart = (int64_t)kRows * (D + 2);  // floats of a partial result
+  static constexpr int64_t kPart = (int64_t)kRows * (D + 3);  // floats of a partial result: sums, maxima, denominators, exponents
 };
 
 // A wait of a whole warp, bounded by its number of tries (it gives up after
@@ -598,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           long long at;            // place of the piece's end in the list
           T* out;
         } old;
-        float m = -INFINITY, l = 0.f;
+        // score and value exponent that the row's weights refer to (their sum, in m alone, up to kFar), denominator
+        float m = -INFINITY, me = 0.f, l = 0.f;
         uint32_t piece_ph = 1;
         for (bool first = true;; first = false) {
           const bool more_pieces = w.left > 0;
@@ -647,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
               if (half == 0) {
                 part[(int64_t)ROWS * D + pr] = m;
                 part[(int64_t)ROWS * D + ROWS + pr] = l;
+                part[(int64_t)ROWS * D + 2 * ROWS + pr] = me;
               }
               // places of the rows' tiles in the list, and the CTAs that hold some of them
               const long long to = old.at + old.to_end, from = to - old.tiles;
@@ -660,11 +666,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
               if (s_last) {
                 __threadfence();
                 auto part_of = [&](int j) { return g.ws + ((int64_t)(c0 + j) * 2 + (j == 0 ? 1 : 0)) * S::kPart; };
-                float top = -INFINITY, sum = 0.f;
-                for (int j = 0; j < n; ++j) top = fmaxf(top, __ldcg(part_of(j) + (int64_t)ROWS * D + pr));
+                float top = -INFINITY, te = 0.f, sum = 0.f;
+                auto max_of = [&](int j) { return __ldcg(part_of(j) + (int64_t)ROWS * D + pr); };
+                auto exp_of = [&](int j) { return __ldcg(part_of(j) + (int64_t)ROWS * D + 2 * ROWS + pr); };
+                for (int j = 0; j < n; ++j) {
+                  const float s = max_of(j), e = exp_of(j);
+                  if ((s - top) + (e - te) > 0.f) top = s, te = e;
+                }
                 const float ref = top == -INFINITY ? 0.f : top;
-                for (int j = 0; j < n; ++j)
-                  sum = fmaf(ex2(__ldcg(part_of(j) + (int64_t)ROWS * D + pr) - ref), __ldcg(part_of(j) + (int64_t)ROWS * D + ROWS + pr), sum);
+                auto weight = [&](int j) { return ex2((max_of(j) - ref) + (exp_of(j) - te)); };
+                for (int j = 0; j < n; ++j) sum = fmaf(weight(j), __ldcg(part_of(j) + (int64_t)ROWS * D + ROWS + pr), sum);
                 const float inv_all = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
                 for (int c = half * kOwnCh; c < (half + 1) * kOwnCh; c += 32) {
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
                   for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                   for (int j = 0; j < n; ++j) {
                     const float* p = part_of(j);
-                    const float f = ex2(__ldcg(p + (int64_t)ROWS * D + pr) - ref);
+                    const float f = weight(j);
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                       const float4 v = __ldcg(reinterpret_cast<const float4*>(p + (int64_t)((c / 4 + u) * ROWS + pr) * 4));
@@ -703,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           row.fq = fmaxf(fabsf(g.a.scale) * kLog2e * exp2i(-up_exponent(row.most)), 1e-22f);
           const int t_begin = w.t, t_end = w.piece_end();
           m = -INFINITY;
+          me = 0.f;
           l = 0.f;
           for (int t = t_begin; t < t_end; ++t, ++k) {
             const int ms = k % kMeta;
@@ -730,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
                   if (c >= n || c < from) x[16 * j + c] = -INFINITY;
               }
             }
-            // scores are f x + e, f and e those of a block
+            // scores are f x, and with them a key weighs f x + e, f and e those of a block
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < kOwn / kBlock; ++j) {
@@ -749,9 +761,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
             }
             // a larger maximum is taken over only where the weights would grow too large
             float keep = 1.f;
-            if (top > m + kSlack || m == -INFINITY) {
-              keep = m == -INFINITY ? 0.f : ex2(m - top);
+            const float held = m + me;
+            const bool more = top > held + kSlack || m == -INFINITY;
+            const float mn = more ? top : m;
+            const bool far = __any_sync(0xFFFFFFFFu, fabsf(mn) > kFar && mn != -INFINITY);
+            if (far) {  // x becomes the difference to the heaviest key's score
+              float bs = -INFINITY, be = 0.f;
+#pragma unroll
+              for (int j = 0; j < kOwn / kBlock; ++j) {
+                const float4 sc = s_scale[ms][blk0 + j];
+                const float f = row.fq * sc.x;
+                float most = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  x[16 * j + c] *= f;
+                  most = fmaxf(most, x[16 * j + c]);
+                }
+                if ((most - bs) + (sc.y - be) > 0.f) bs = most, be = sc.y;
+              }
+              if (kHalves) {  // both threads of a row choose alike, the larger score where two keys weigh the same
+                float s2, e2;
+                if (!other_half(bs, s2) || !other_half(be, e2)) break;
+                const float over = (s2 - bs) + (e2 - be);
+                if (over > 0.f || (over == 0.f && s2 > bs)) bs = s2, be = e2;
+              }
+              if ((bs - m) + (be - me) > kSlack) {
+                keep = m == -INFINITY ? 0.f : ex2((m - bs) + (me - be));
+                m = bs;
+                me = be;
+              }
+              const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+              for (int c = 0; c < kOwn; ++c) x[c] -= from;
+            } else if (more) {
+              keep = m == -INFINITY ? 0.f : ex2((m - top) + me);
               m = top;
+              me = 0.f;
             }
             auto used = [&]() {  // the weights of the tile before, and with them its sums
               if (t > t_begin) ok = wait_warp(o_full(q), (k - 1) & 1, abort_flag, 53);
@@ -773,12 +818,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
                 tmem_store(o_at + c, y);
               }
             }
-            const float ref = (m == -INFINITY ? 0.f : m) - kPUp;
+            const float ref = (far || m == -INFINITY ? 0.f : m) + (me - kPUp);
             uint32_t p[kOwn / 2];
 #pragma unroll
             for (int j = 0; j < kOwn / kBlock; ++j) {
               const float4 sc = s_scale[ms][blk0 + j];
-              const float fj = row.fq * sc.x, ej = sc.y - ref;
+              const float fj = far ? 1.f : row.fq * sc.x, ej = sc.y - ref;
               float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {

@@ -32,7 +32,7 @@ def absolute_values(s):
 # Softmax weights are rounded to f16 (2^-12 of each) and the sums to f32, for which 2^-11 leaves room.
 @pytest.mark.parametrize("dim,dt", SIZES)
 @pytest.mark.parametrize("score", [2.0**12.1, 2.0**20.4, 2.0**24.7, 2.0**26.3, 2.0**27.9, 2.0**30.2])
-@pytest.mark.parametrize("new", [1, 2])
+@pytest.mark.parametrize("new", [1, 2, 60])
 def test_large_scores_of_equal_keys(nv, dim, dt, score, new):  # noqa: F811
     """Some keys score the same, all others at least a fourteenth less: the mean of the former's values, whatever the
     scales of the blocks that they lie in, at any size of the scores (in the exponent of 2)."""
@@ -54,7 +54,7 @@ def test_large_scores_of_equal_keys(nv, dim, dt, score, new):  # noqa: F811
 
 @pytest.mark.parametrize("dim,dt", SIZES)
 @pytest.mark.parametrize("score", [2.0**24.2, 2.0**25.6, 2.0**26.9, 2.0**28.5, 2.0**30.1])
-@pytest.mark.parametrize("new", [1, 2])
+@pytest.mark.parametrize("new", [1, 2, 60])
 def test_large_scores_close_together(nv, dim, dt, score, new):  # noqa: F811
     """Scores a few units of their last place apart, growing and falling from tile to tile: which key is heaviest is a
     matter of rounding, but a result lies between the smallest and the largest value."""
