@@ -710,8 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
             if (!wait_warp(q_full(q), piece_ph, abort_flag, 52)) break;
             row.most = (uint32_t)s_most[r] << 23;
           }
-          // (never zero, not even times a block's scale: a masked key's minus infinity has to stay one)
-          row.fq = fmaxf(fabsf(g.a.scale) * kLog2e * exp2i(-up_exponent(row.most)), 1e-22f);
+          // Never zero, not even times a block's scale (2^-48 at least): a masked key's minus infinity has to stay one. A
+          // factor that is raised to 2^-98 gives scores below 2^-25 with any keys (products below 2^25 times 2^48).
+          row.fq = fmaxf(fabsf(g.a.scale) * kLog2e * exp2i(-up_exponent(row.most)), exp2i(-98));
           const int t_begin = w.t, t_end = w.piece_end();
           m = -INFINITY;
           me = 0.f;

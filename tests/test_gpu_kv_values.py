@@ -71,3 +71,20 @@ def test_large_scores_close_together(nv, dim, dt, score, new):  # noqa: F811
     y, most, least = y.double().cpu().numpy(), v.max((0, 1)), v.min((0, 1))
     slack = (2.0**-11 + HALF_ULP[dt]) * np.abs(v).max((0, 1))
     assert np.isfinite(y).all() and (y <= most + slack).all() and (y >= least - slack).all()
+
+
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("up,scale", [(1.0, 1e-20), (1.0, -1e-24), (1.0, 1e-38), (1.0, 0.0), (1e-22, 0.1), (1e-30, 0.1)])
+def test_small_factors_of_large_keys(nv, dim, dt, new, up, scale):  # noqa: F811
+    """Keys at the top of their range along the queries or against them, under factors that make the scores small."""
+    if dt == "f16" and up < 1.0:
+        up, scale = 2.0**-20, scale * up * 2.0**20  # the same product: f16 has no smaller queries
+    s = Step(nv, 52, [new], [700], 2, 1, dim, 64, dt)
+    s.cache[2][:] = 127 + 48
+    set_keys(s, s.g.choice([-448.0, 448.0], size=int(s.lengths[0])) * 2.0**48)
+    q = torch.full((new, 2, dim), 1.9 * up).to(DT[dt])
+    _, ref, bound = s.attend(q, scale=scale)
+    mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, scale)
+    assert (bound <= 2.0**-10 * mean).all()  # scores a thousandth too large would not pass
+    s.check(q, scale=scale)
