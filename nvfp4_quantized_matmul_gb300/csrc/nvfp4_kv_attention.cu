@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1));
         bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 2));
         // largest magnitude into [2^7, 2^8); a row with a value that is not finite becomes no number
-        const int up_e = min(7 - max((int)(bits >> 23) - 127, -100), 100);
+        const int up_e = min(7 - ((int)(bits >> 23) - 127), 126);
         const float up = bits < 0x7F800000u ? exp2i(up_e) : __int_as_float(0x7FC00000);
         fq[h] = g.a.scale * kLog2e * exp2i(-up_e);
 #pragma unroll

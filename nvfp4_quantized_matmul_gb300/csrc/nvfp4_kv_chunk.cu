@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           float fq;       // scale of its scores, with the logarithm's base and the queries' power of two
           T* out;
         };
-        auto up_exponent = [](uint32_t bits) { return min(7 - max((int)(bits >> 23) - 127, -100), 100); };
+        auto up_exponent = [](uint32_t bits) { return min(7 - ((int)(bits >> 23) - 127), 126); };
         // this thread's row of the piece; the warp's queries as terms in swizzled rows
         auto queries = [&](Row& row) {
           const Item& it = w.it;

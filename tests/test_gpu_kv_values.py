@@ -88,3 +88,18 @@ def test_small_factors_of_large_keys(nv, dim, dt, new, up, scale):  # noqa: F811
     mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, scale)
     assert (bound <= 2.0**-10 * mean).all()  # scores a thousandth too large would not pass
     s.check(q, scale=scale)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("up,scale", [(1e-26, 1e34), (1e-30, 1e37), (1e-34, 2e38)])
+def test_small_queries(nv, dim, new, up, scale):  # noqa: F811
+    """Rows whose largest query is near bf16's smallest, under a scale that makes their scores count."""
+    s = Step(nv, 55, [new], [300], 2, 1, dim, 64, "bf16")
+    s.cache[2][:] = 127 - 8 - int(round(np.log2(up * scale)))
+    s.load()
+    q = s.rows(2, up)
+    _, ref, bound = s.attend(q, scale=scale)
+    mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, scale)
+    assert (bound <= 0.05 * mean).all()
+    s.check(q, scale=scale)
