@@ -50,6 +50,14 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// What a row's products are multiplied by, apart from the blocks' scales, to give scores in the exponent of 2: queries are
+// held times 2^up_e. Times a block's scale it stays below 2^128, so that a key of zeros scores zero and not no number; a
+// factor beyond 2^79 leaves scores that differ at all further apart than any weight reaches.
+__device__ __forceinline__ float score_factor(float scale, int up_e) {
+  const float f = (scale * exp2i(-up_e)) * 1.4426950408889634f, most = exp2i(79);
+  return fminf(fmaxf(f, -most), most);
+}
+
 // Two values -> two E4M3 codes (lo in the low byte), nearest, ties to even,
 // saturating at 448; NaN gives 0x7F.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

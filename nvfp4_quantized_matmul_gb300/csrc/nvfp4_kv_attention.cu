@@ -62,7 +62,6 @@ using namespace pipe;
 
 __device__ int g_kv_error = 0;  // first error code recorded by a bounded wait
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 64;      // tokens a tile
 // Tiles a CTA takes at least: 40 sequences of up to 300 keys, 24 / 2 heads, take 11.2 us with 1 to 4, 12.8 with 8 and 18.6
 // with 16; one of 3000 keys, 32 / 8 heads, 13.3, 14.1 and 17.7.
@@ -451,7 +450,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         // largest magnitude into [2^7, 2^8); a row with a value that is not finite becomes no number
         const int up_e = min(7 - ((int)(bits >> 23) - 127), 126);
         const float up = bits < 0x7F800000u ? exp2i(up_e) : __int_as_float(0x7FC00000);
-        fq[h] = g.a.scale * kLog2e * exp2i(-up_e);
+        fq[h] = score_factor(g.a.scale, up_e);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {  // step c
             const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};

@@ -47,7 +47,6 @@ using namespace pipe;
 
 __device__ int g_chunk_error = 0;  // first error code recorded by a bounded wait
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kPanel = 64;       // tokens of a panel of converted values: rows of 128 bytes
 constexpr float kPUp = 7.0f;     // the weights are held times 2^7
@@ -712,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           }
           // Never zero, not even times a block's scale (2^-48 at least): a masked key's minus infinity has to stay one. A
           // factor that is raised to 2^-98 gives scores below 2^-25 with any keys (products below 2^25 times 2^48).
-          row.fq = fmaxf(fabsf(g.a.scale) * kLog2e * exp2i(-up_exponent(row.most)), exp2i(-98));
+          row.fq = fmaxf(score_factor(fabsf(g.a.scale), up_exponent(row.most)), exp2i(-98));
           const int t_begin = w.t, t_end = w.piece_end();
           m = -INFINITY;
           me = 0.f;

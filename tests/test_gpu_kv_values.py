@@ -103,3 +103,38 @@ def test_small_queries(nv, dim, new, up, scale):  # noqa: F811
     mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, scale)
     assert (bound <= 0.05 * mean).all()
     s.check(q, scale=scale)
+
+
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("new", [1, 60])
+def test_large_factors_of_small_keys(nv, dim, dt, new):  # noqa: F811
+    """A scale near f32's largest, whose product with log2 e is beyond it: moderate scores of small queries and keys."""
+    up, e = (1e-30, -33) if dt == "bf16" else (2.0**-20, -48)
+    scale = 3e38 if dt == "bf16" else 3e18
+    s = Step(nv, 53, [new], [300], 2, 1, dim, 64, dt)
+    s.cache[2][:] = 127 + e
+    s.load()
+    q = s.rows(2, up)
+    _, ref, bound = s.attend(q, scale=scale)
+    mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, scale)
+    assert (bound <= 0.1 * mean).all()
+    s.check(q, scale=scale)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 60])
+def test_large_factors_of_large_queries(nv, dim, new):  # noqa: F811
+    """Queries near bf16's largest under a large scale: the factor of the products is beyond f32, the scores are not. The
+    heaviest keys' mean; a key of zeros scores zero."""
+    s = Step(nv, 54, [new], [700], 2, 1, dim, 64, "bf16")
+    length = int(s.lengths[0])
+    s.cache[2][:] = 127 - 48
+    values = s.g.choice([-1.0, 0.0, 0.5], size=length)
+    values[s.g.choice(length, size=20, replace=False)] = 1.75
+    values[:3] = 1.75
+    set_keys(s, values * 2.0**-40)
+    q = torch.full((new, 2, dim), 2.0**126, dtype=torch.bfloat16)
+    y, ref, _ = s.attend(q, scale=1000.0)
+    mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, 1000.0)
+    lim = 2.0**-11 * mean + HALF_ULP["bf16"] * np.abs(ref)
+    assert (np.abs(y.double().cpu().numpy() - ref) <= lim).all()
