@@ -30,10 +30,12 @@
 // in the same order.
 //
 // q . k runs on the f8 tensor instructions with the codes as they lie: a
-// query row is scaled by a power of two and split into E4M3 terms (a bf16
-// value is exactly two of them, an f16 value three; each further term scaled
-// up by 16), which costs a fourth of the f16 instructions and no conversion
-// of keys. Up to eight rows, the first two terms are the upper and lower
+// query row is scaled by a power of two and split into E4M3 terms (two for
+// bf16, three for f16; each further term scaled up by 16), which costs a
+// fourth of the f16 instructions and no conversion of keys. The terms' sum is
+// exact for queries down to 2^-13 of the row's largest and within 2^-21
+// (bf16) or 2^-25 (f16) of it below that, where the first term ends at E4M3's
+// smallest step. Up to eight rows, the first two terms are the upper and lower
 // half of one 16-row operand. The weights p are rounded to f16 (scaled by
 // 2^14, so that a key counts until it is 2^38 lighter than the heaviest) and
 // multiply values converted to f16, which is exact; the values are the

@@ -5,9 +5,13 @@
 // 128 query rows (token, head of the group) of one key/value head and walks
 // the visible tiles of 128 keys:
 //   S = Q K^T   kind::f8f6f4: a query row, scaled by a power of two, is the
-//               exact sum of two (bf16) or three (f16) E4M3 terms, each one
-//               product with the key codes as they lie in the cache, whose
-//               pages are the swizzled operand; no key is converted
+//               sum of an E4M3 term and one (bf16) or two (f16) E5M2 terms,
+//               each one product with the key codes as they lie in the
+//               cache, whose pages are the swizzled operand; no key is
+//               converted. The sum is exact for queries down to 2^-13 of the
+//               row's largest, and within 2^-21 (bf16) or 2^-24 (f16) of it
+//               below that: further terms in E4M3 would share the first
+//               one's smallest step of 2^-9 and end at 2^-17
 //   P = 2^(t - m) in f16, written over S
 //   O += P V    kind::f16: P from TMEM, values converted to f16 (exactly)
 // Bound by the tensor cores where a chunk is long: 2048 tokens at 14000 keys
@@ -130,7 +134,8 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
   constexpr uint64_t mode = W == 128 ? 2 : 4;
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(8 * W >> 4) << 32) | ((uint64_t)1 << 46) | (mode << 61);
 }
-// f32 accumulator, M = 128, both operands K-major; E4M3 and f16 are format 0 of their kinds.
+// f32 accumulator, M = 128, both operands K-major; E4M3 and f16 are format 0 of their kinds, E5M2 is format 1 (of A, bit 7).
+constexpr uint32_t kE5m2Queries = 1u << 7;
 __host__ __device__ constexpr uint32_t instruction(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -210,6 +215,14 @@ __device__ __forceinline__ uint32_t e4m3x2_of(__half2 x) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
   return r;
 }
+
+__device__ __forceinline__ uint32_t e5m2x2_of(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+// An E5M2 code is the upper byte of the f16 it stands for.
+__device__ __forceinline__ __half2 half2_of_e5m2x2(uint32_t codes) { return as_half2(__byte_perm(codes, 0, 0x1404)); }
 
 // Two f32 operations an instruction, and the maximum of three.
 __device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
@@ -549,11 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
                 uint32_t code[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                  const uint32_t c0 = e4m3x2_of(v[2 * j]), c1 = e4m3x2_of(v[2 * j + 1]);
+                  const uint32_t c0 = n == 0 ? e4m3x2_of(v[2 * j]) : e5m2x2_of(v[2 * j]);
+                  const uint32_t c1 = n == 0 ? e4m3x2_of(v[2 * j + 1]) : e5m2x2_of(v[2 * j + 1]);
                   code[j] = c0 | (c1 << 16);
                   if (n < TERMS - 1) {
-                    v[2 * j] = __hsub2(v[2 * j], as_half2(e4m3x2_to_f16x2(c0)));
-                    v[2 * j + 1] = __hsub2(v[2 * j + 1], as_half2(e4m3x2_to_f16x2(c1)));
+                    v[2 * j] = __hsub2(v[2 * j], n == 0 ? as_half2(e4m3x2_to_f16x2(c0)) : half2_of_e5m2x2(c0));
+                    v[2 * j + 1] = __hsub2(v[2 * j + 1], n == 0 ? as_half2(e4m3x2_to_f16x2(c1)) : half2_of_e5m2x2(c1));
                   }
                 }
                 asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(code[0]), "r"(code[1]) : "memory");
@@ -1043,8 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
               for (int p = 0; p < S::kPanels; ++p)
 #pragma unroll
                 for (int s = 0; s < S::W / 32; ++s)
-                  mma_f8(tmem, qt + (n * S::kQTerm + p * (128 * S::W) + 32 * s) / 16, kt + (p * (kKeys * S::W) + 32 * s) / 16, idesc,
-                         n < TERMS - 1 || p > 0 || s > 0);
+                  mma_f8(tmem, qt + (n * S::kQTerm + p * (128 * S::W) + 32 * s) / 16, kt + (p * (kKeys * S::W) + 32 * s) / 16,
+                         n > 0 ? idesc | kE5m2Queries : idesc, n < TERMS - 1 || p > 0 || s > 0);
             tc_commit(s_full(q));
             if (q == NQ - 1) tc_commit(k_empty(ks));
           }

@@ -138,3 +138,41 @@ def test_large_factors_of_large_queries(nv, dim, new):  # noqa: F811
     mean, _ = K.attention(q.double().numpy(), absolute_values(s), s.table, s.lengths, s.offsets, 1000.0)
     lim = 2.0**-11 * mean + HALF_ULP["bf16"] * np.abs(ref)
     assert (np.abs(y.double().cpu().numpy() - ref) <= lim).all()
+
+
+def query_bound(s, q, scale, kept):
+    """Bound on the results where queries down to 2^-13 of a row's largest are held as they are and smaller ones to
+    `kept` of it: weights in f16, sums in f32."""
+    out = np.zeros(q.shape)
+    for b, length in enumerate(s.lengths):
+        k, v, _ = K.dense(s.cache, s.table[b], int(length))
+        for i in range(int(s.new[b])):
+            n = int(length - s.new[b]) + i + 1
+            for h in range(s.heads):
+                kh, vh, row = k[:n, h * s.kv_heads // s.heads], v[:n, h * s.kv_heads // s.heads], q[s.offsets[b] + i, h]
+                big = np.abs(row).max()
+                err = np.where(np.abs(row) >= big * 2.0**-13, 0.0, np.minimum(kept * big, np.abs(row)))
+                w = np.exp((kh @ row) * scale - ((kh @ row) * scale).max())
+                ds = abs(scale) * (np.abs(kh) @ err + np.abs(kh) @ np.abs(row) * s.dim * 2.0**-24).max()
+                out[s.offsets[b] + i, h] = (np.abs(vh).T @ (w / w.sum())) * (2.0**-11 + 2 * np.expm1(ds) + n**0.5 * 2.0**-23)
+    return out
+
+
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("new", [[1], [2, 1], [60], [130]])
+@pytest.mark.parametrize("outlier,ones", [(30.0, False), (1000.0, False), (1000.0, True), (8000.0, False), (8000.0, True), (60000.0, False)])
+def test_queries_with_one_large_channel(nv, dim, dt, new, outlier, ones):  # noqa: F811
+    """One channel of a query far larger than the rest, and no key that uses it: the others' products keep their precision,
+    and down to 2^-13 of the largest (`ones`: magnitudes from 1 to 2) they lose nothing."""
+    s = Step(nv, 56, new, [200] * len(new), 2, 1, dim, 32, dt)
+    places = K.key_places(dim)
+    s.cache[0][..., places[:, 5]] = 0
+    s.load()
+    q = s.rows(2)
+    if ones:
+        q = torch.sign(q) * (1 + torch.from_numpy(s.g.integers(0, 128, size=tuple(q.shape)) / 128.0)).to(q.dtype)
+    q[..., 5] = outlier
+    y, ref, _ = s.attend(q, scale=0.4)
+    lim = query_bound(s, q.double().numpy(), 0.4, 2.0**-21 if dt == "bf16" else 2.0**-24) + HALF_ULP[dt] * np.abs(ref)
+    err = np.abs(y.double().cpu().numpy() - ref)
+    assert (err <= lim + (2.0**-24 if dt == "f16" else 0.0)).all(), float((err / lim).max())
