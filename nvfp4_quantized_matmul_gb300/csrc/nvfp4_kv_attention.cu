@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
       for (int h = 0; h < H; ++h) {
         const int row = out.rt * ROWS + gr + 8 * h, i = row / group;
         const bool ok = i < sq.n;
-        pos[h] = ok ? start + i : -1;
-        low[h] = g.a.window > 0 ? (int)max((int64_t)pos[h] - g.a.window + 1, (int64_t)0) : 0;
+        pos[h] = ok ? start + i : 0x3FFFFFFF;  // no row: beyond any token, so that it needs no mask
+        low[h] = ok && g.a.window > 0 ? (int)max((int64_t)pos[h] - g.a.window + 1, (int64_t)0) : 0;
         m[h] = -INFINITY;
         me[h] = 0.f;
         l[h] = 0.f;
@@ -484,11 +484,10 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
           }
       }
       __syncwarp();
-      // rows there are, for the test whether a tile needs a mask
-      int lo_pos = 0x7FFFFFFF, hi_low = 0;
+      // for the test whether a tile needs a mask (a row before the sequence's first token sees none of its keys)
+      int lo_pos = pos[0], hi_low = low[0];
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (pos[h] >= 0) lo_pos = min(lo_pos, pos[h]), hi_low = max(hi_low, low[h]);
+      for (int h = 1; h < H; ++h) lo_pos = min(lo_pos, pos[h]), hi_low = max(hi_low, low[h]);
       pos_min = __reduce_min_sync(0xFFFFFFFFu, lo_pos);
       low_max = __reduce_max_sync(0xFFFFFFFFu, hi_low);
 #pragma unroll

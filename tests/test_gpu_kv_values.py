@@ -176,3 +176,14 @@ def test_queries_with_one_large_channel(nv, dim, dt, new, outlier, ones):  # noq
     lim = query_bound(s, q.double().numpy(), 0.4, 2.0**-21 if dt == "bf16" else 2.0**-24) + HALF_ULP[dt] * np.abs(ref)
     err = np.abs(y.double().cpu().numpy() - ref)
     assert (err <= lim + (2.0**-24 if dt == "f16" else 0.0)).all(), float((err / lim).max())
+
+
+@pytest.mark.parametrize("new,ctx", [([90], [-26]), ([96, 2], [-32, 100]), ([40, 80], [-40, -16]), ([300], [-100]), ([150, 1], [-22, 5])])
+@pytest.mark.parametrize("heads,kv_heads,dim,window", [(1, 1, 64, 0), (2, 2, 64, 30), (2, 2, 128, 0), (4, 2, 256, 0)])
+def test_more_new_tokens_than_the_length(nv, new, ctx, heads, kv_heads, dim, window):  # noqa: F811
+    """Rows before a sequence's first token see no key and give zeros, also where whole tiles of rows are such."""
+    s = Step(nv, 57, new, ctx, heads, kv_heads, dim, 16, "bf16")
+    y = s.check(s.rows(heads), window=window)
+    for b, c in enumerate(ctx):
+        if c < 0:
+            assert (y[int(s.offsets[b]):int(s.offsets[b]) - c] == 0).all()
