@@ -32,6 +32,10 @@
  *     nvfp4_shutdown(). Made while the stream is being captured into a CUDA
  *     graph, the allocation is done outside the capture (the thread's capture
  *     mode relaxed for it) and the graph uses that memory on every replay.
+ *     So graphs captured on one stream share its scratch, with one another
+ *     and with that stream's own calls: they must not run at the same time.
+ *     The cache attention's alone is safe there: each capture has its own
+ *     (see nvfp4_kv_attention).
  *   - Data pointers must be 16-byte aligned; index arrays and gs 4-byte.
  *   - K must be a multiple of 16. Any N >= 1 is accepted.
  *   - Empty outputs (M, N or R equal to 0) return NVFP4_OK without a launch.
@@ -415,7 +419,12 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const nvfp4_kv_batch* 
  *   of any one sequence, which chooses between kernels.
  * Products and sums are taken in f32, the softmax's weights rounded to f16
  * before the second product. Scratch: partial results of up to two parts of a
- * head per SM and one per warp (5 to 41 MB on 152 SMs), per (device, stream).
+ * head per SM and one per warp (5 to 41 MB on 152 SMs), per (device, stream),
+ * the per-thread default stream counting as one for each thread. Calls that
+ * are captured into a graph have their own, one for each stream of a capture;
+ * once every graph made from it is destroyed, a later capture may use it.
+ * Graphs of different captures may run at the same time, two instances of one
+ * capture's graph may not.
  */
 nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_batch* batch, nvfp4_dtype dtype, const void* q,
                                 int64_t q_stride, int64_t heads, int64_t max_q, float scale, int64_t window, void* out,

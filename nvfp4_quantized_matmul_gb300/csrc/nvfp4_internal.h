@@ -176,10 +176,9 @@ cudaError_t launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAtte
 cudaError_t launch_kv_chunk(const KvCache& c, const KvBatch& b, const KvAttention& a, int few, int dtype, cudaStream_t st);
 int read_kv_error();
 int read_kv_chunk_error();
-// Scratch of both attention kernels, one allocation per (device, stream),
-// made on the first call that needs it, grown on demand, kept until
-// release_kv_workspaces(): arrival counts (zero between calls) and partial
-// results.
+// Scratch of both attention kernels, one allocation per (device, stream) and
+// one per stream of a graph capture, made on the first call that needs it,
+// grown on demand: arrival counts (zero between calls) and partial results.
 constexpr int kKvMaxCtas = 512;
 cudaError_t kv_workspace(int dev, cudaStream_t st, size_t bytes, unsigned** done, float** parts);
 void release_kv_workspaces();
