@@ -431,8 +431,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_batc
                                 int64_t out_stride, void* stream);
 
 /* Error code recorded on the device by a pipelined kernel whose bounded
- * wait on a pipeline barrier ran out (each wait gives up after 2 s instead of
- * hanging, and the kernel then returns without finishing its tiles); the
+ * wait on a pipeline barrier ran out (each wait gives up after about 2 s
+ * instead of hanging, and the kernel then returns without finishing its tiles); the
  * call reads and clears it (and, after an error, clears the decode
  * workspaces). Blocks until all prior work on the current device
  * has finished. Returns 0 when no wait gave up, -1 if the read failed. Not
@@ -468,11 +468,13 @@ typedef enum {
                                    tensor-core route wherever supported; 0: never */
   NVFP4_OPT_GATHER_TILE = 7,    /* expert-batched route's tile: 0 automatic (default, 256x256), 1 256x256,
                                    2 256x128, 3 128x256 */
-  NVFP4_OPT_WAIT_LIMIT_US = 8,  /* decode-route calls of nvfp4_qmm: limit of each bounded wait in
-                                   microseconds, 0 (default) for 2 s; for tests of the stall path */
+  NVFP4_OPT_WAIT_LIMIT_US = 8,  /* decode-route calls of nvfp4_qmm, and nvfp4_kv_attention: limit of each
+                                   bounded wait in microseconds, 0 (default) for 2 s; for tests of
+                                   the stall path */
   NVFP4_OPT_TEST_WITHHOLD = 9   /* tests of the stall path only: 1 makes the first CTA of the next
                                    decode-route nvfp4_qmm launches withhold the release of one
-                                   pipeline stage, so that a bounded wait runs out (the call then
+                                   pipeline stage, and every second CTA of nvfp4_kv_attention's wait
+                                   for one arrival too many, so that a bounded wait runs out (the call then
                                    reports its error code through nvfp4_take_device_error and
                                    leaves no copy in flight); 0 (default) off */
 } nvfp4_option;

@@ -93,6 +93,18 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float up) {
   return e4m3x4(a.x * up, a.y * up, b.x * up, b.y * up);
 }
 
+// Limit of every wait of a call's kernels (2 s unless a test shortens it), and, for tests of that limit only, a flag that
+// keeps every second CTA's first tile of keys from being seen to arrive, so that a wait runs out.
+struct Waits {
+  uint32_t limit_ns;
+  int withhold;
+  __device__ __forceinline__ uint32_t stalls() const { return withhold && blockIdx.x % 2 == 0 ? 1 : 0; }
+};
+inline Waits waits() {
+  const int us = option(kOptWaitLimitUs);
+  return Waits{us > 0 ? (uint32_t)us * 1000u : 2000000000u, option(kOptTestWithhold)};
+}
+
 // New tokens and tokens in all of sequence b, made safe against offsets that
 // do not fit: first .. first + n lie within [0, tokens], n <= length.
 struct Seq {

@@ -86,6 +86,7 @@ struct AttnArgs {
   KvCache c;
   KvBatch b;
   KvAttention a;
+  Waits waits;
   int few;         // sequences of more rows are the other kernel's
   float* ws;       // partial results: 2 a CTA, then 1 a warp
   unsigned* done;  // [CTAs] arrivals at the head that starts in a CTA and goes on after it; zero between calls
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
   const int seqs = (int)g.b.seqs, group = (int)g.a.group;
 
   if (lane == 0) {  // a warp's barriers are its own
-    mbar_init(smem_addr(&s_bar[2 * warp]), 1);
+    mbar_init(smem_addr(&s_bar[2 * warp]), 1 + (warp == 0 ? g.waits.stalls() : 0));
     mbar_init(smem_addr(&s_bar[2 * warp + 1]), 1);
     s_abort[warp] = 0;
     s_piece[2 * warp].at = s_piece[2 * warp + 1].at = nullptr;
@@ -690,17 +691,17 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
       const int tok0 = (out.w.t0 + out.tile) * kTile, k_e = ek, v_e = ev;
       const uint32_t blocks = there;
       const bool clean = blocks == 0xFu && tok0 + kTile - 1 <= pos_min && tok0 >= low_max;
-      bool ok = wait_bar_warp(bar_k, it & 1, abort_flag, 41, &g_kv_error);
+      bool ok = wait_bar_warp(bar_k, it & 1, abort_flag, 41, &g_kv_error, g.waits.limit_ns);
       if (ok) {
         scores();
         __syncwarp();
         if (it + 1 < count) copy_keys();
         weights(tok0, k_e, v_e, blocks, clean);
-        ok = wait_bar_warp(bar_v, it & 1, abort_flag, 42, &g_kv_error);
-        if (!ok && it + 1 < count) wait_bar_quiet(bar_k, (it + 1) & 1);
+        ok = wait_bar_warp(bar_v, it & 1, abort_flag, 42, &g_kv_error, g.waits.limit_ns);
+        if (!ok && it + 1 < count) wait_bar_quiet(bar_k, (it + 1) & 1, g.waits.limit_ns);
       } else {
-        wait_bar_quiet(bar_k, it & 1);
-        wait_bar_quiet(bar_v, it & 1);
+        wait_bar_quiet(bar_k, it & 1, g.waits.limit_ns);
+        wait_bar_quiet(bar_v, it & 1, g.waits.limit_ns);
       }
       if (!ok) break;  // the copies in flight have landed or been given up on
       if (!clean) clear_tail(tok0, blocks);
@@ -904,8 +905,8 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         }
         __syncthreads();
       }
-      ok = wait_bar_warp(bar_join, joins & 1, abort_flag, 43, &g_kv_error);
-      if (!ok) wait_bar_quiet(bar_join, joins & 1);
+      ok = wait_bar_warp(bar_join, joins & 1, abort_flag, 43, &g_kv_error, g.waits.limit_ns);
+      if (!ok) wait_bar_quiet(bar_join, joins & 1, g.waits.limit_ns);
       ok = __syncthreads_and(ok);
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
@@ -1080,7 +1081,7 @@ cudaError_t launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAtte
     const cudaError_t e = launch_kv_chunk(c, b, a, all ? 0 : few, dtype, st);
     if (e != cudaSuccess || all) return e;
   }
-  const AttnArgs g{c, b, a, chunks ? few : 0x7FFFFFFF, nullptr, nullptr};
+  const AttnArgs g{c, b, a, waits(), chunks ? few : 0x7FFFFFFF, nullptr, nullptr};
   return dtype == kBF16 ? launch_t<__nv_bfloat16>(g, st) : launch_t<__half>(g, st);
 }
 

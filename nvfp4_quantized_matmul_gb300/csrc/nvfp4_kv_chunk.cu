@@ -73,6 +73,7 @@ struct ChunkArgs {
   KvCache c;
   KvBatch b;
   KvAttention a;
+  Waits waits;
   int few;         // sequences of up to so many rows are the other kernel's
   float* ws;       // partial results, two a CTA
   unsigned* done;  // [CTAs] arrivals at the rows that start in a CTA and go on after it; zero between calls
@@ -96,11 +97,10 @@ struct Shape {
   static constexpr int64_t kPart = (int64_t)kRows * (D + 3);  // floats of a partial result: sums, maxima, denominators, exponents
 };
 
-// A wait of a whole warp, bounded by its number of tries (it gives up after
-// some tenths of a second): less code than a wait with a clock, and the
-// roles' loops have to share the instruction cache. Without a time to be
-// suspended for, a try returns sooner.
-constexpr uint32_t kTries = 1u << 23;
+// A wait of a whole warp, bounded by its number of tries. Each lasts up to 3.75 us (measured: the hardware suspends the
+// warp meanwhile), so the limit is about the call's in time. Looking at a clock every 256 tries takes more code, and the
+// roles' loops have to share the instruction cache: a prompt of 8192 tokens then takes 463 us, with the count 412.
+constexpr uint32_t kNsATry = 3750;
 __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -110,13 +110,20 @@ __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int code, uint32_t bar2 = 0, uint32_t parity2 = 0) {
-  for (uint32_t n = 0; !__all_sync(0xFFFFFFFFu, try_bar(bar, parity) & (bar2 == 0 || try_bar(bar2, parity2))); ++n) {
-    if ((n & 255) == 255 && (*abort_flag || n > kTries)) {
-      if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) atomicCAS(&g_chunk_error, 0, code);
+// Tries that a wait is given, and the CTA's flag that one has run out.
+struct Limit {
+  int* abort_flag;
+  uint32_t tries;
+  __device__ __forceinline__ void give_up(int code) const {
+    if (atomicExch(abort_flag, 1) == 0) atomicCAS(&g_chunk_error, 0, code);
+  }
+};
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Limit& limit, int code, uint32_t bar2 = 0, uint32_t parity2 = 0) {
+  for (uint32_t n = 0; !__all_sync(0xFFFFFFFFu, try_bar(bar, parity) & (bar2 == 0 || try_bar(bar2, parity2))); ++n)
+    if (n > limit.tries) {
+      limit.give_up(code);
       return false;
     }
-  }
   return true;
 }
 
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(k_full(s), 1);
+      mbar_init(k_full(s), 1 + g.waits.stalls());
       mbar_init(k_empty(s), 1);
       mbar_init(q_full(s), NQ == 1 && s == 1 ? 2 : 8 / NQ);
       mbar_init(s_full(s), NQ == 1 && s == 1 ? 2 : 1);
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
     if (lane == 0) s_walk = w;
   }
   __syncthreads();
-  volatile int* abort_flag = &s_abort;
+  const Limit limit{&s_abort, g.waits.limit_ns / kNsATry};
 
   if (at0 < at1) {
     Walk<ROWS> w = s_walk;
@@ -594,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
         auto meet = [&]() {  // all softmax warps; bounded, unlike a named barrier
           __syncwarp();
           if (lane == 0) mbar_arrive(joined);
-          ok = wait_warp(joined, meets++ & 1, abort_flag, 63);
+          ok = wait_warp(joined, meets++ & 1, limit, 63);
           return ok;
         };
         uint32_t pairs = 0;
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           *at = mine;
           __syncwarp();
           if (lane == 0) mbar_arrive(pair_bar(warp & 3));
-          ok = wait_warp(pair_bar(warp & 3), pairs++ & 1, abort_flag, 56);
+          ok = wait_warp(pair_bar(warp & 3), pairs++ & 1, limit, 56);
           other = at[half ? -128 : 128];
           return ok;
         };
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           Row row;
           if (more_pieces) queries(row);
           if (!first) {
-            if (!wait_warp(o_full(q), (k - 1) & 1, abort_flag, 54)) {
+            if (!wait_warp(o_full(q), (k - 1) & 1, limit, 54)) {
               ok = false;
               break;
             }
@@ -720,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           }
           if (!more_pieces) break;
           if (kHalves) {
-            if (!wait_warp(q_full(q), piece_ph, abort_flag, 52)) break;
+            if (!wait_warp(q_full(q), piece_ph, limit, 52)) break;
             row.most = (uint32_t)s_most[r] << 23;
           }
           // Never zero, not even times a block's scale (2^-48 at least): a masked key's minus infinity has to stay one. A
@@ -732,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           l = 0.f;
           for (int t = t_begin; t < t_end; ++t, ++k) {
             const int ms = k % kMeta;
-            if (!wait_warp(meta_full(ms), (k / kMeta) & 1, abort_flag, 51, s_full(q), k & 1)) {
+            if (!wait_warp(meta_full(ms), (k / kMeta) & 1, limit, 51, s_full(q), k & 1)) {
               ok = false;
               break;
             }
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
               me = 0.f;
             }
             auto used = [&]() {  // the weights of the tile before, and with them its sums
-              if (t > t_begin) ok = wait_warp(o_full(q), (k - 1) & 1, abort_flag, 53);
+              if (t > t_begin) ok = wait_warp(o_full(q), (k - 1) & 1, limit, 53);
               tc_after();
               return ok;
             };
@@ -878,8 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
       for (int p = 0; w.left > 0; ++p, w.advance(g, w.t + ((p & 1) ^ 1))) {
         const int s = p % S::kSlots;
         const uint32_t ph = (p / S::kSlots) & 1;
-        if (!wait_warp(raw_full(s), ph, abort_flag, 55, val_empty(s), ph ^ 1)) break;
-        if (kTwoCopiers && (p & 1) == 0 && !wait_warp(meta_full((p >> 1) % kMeta), ((p >> 1) / kMeta) & 1, abort_flag, 59)) break;
+        if (!wait_warp(raw_full(s), ph, limit, 55, val_empty(s), ph ^ 1)) break;
+        if (kTwoCopiers && (p & 1) == 0 && !wait_warp(meta_full((p >> 1) % kMeta), ((p >> 1) / kMeta) & 1, limit, 59)) break;
         const uint32_t src = raw_at + s * S::kRaw, dst = val_at + s * S::kVal;
         const float4* of_blocks = &s_scale[(p >> 1) % kMeta][4 * (p & 1)];
         const int4 valid = make_int4(__float_as_int(of_blocks[0].w), __float_as_int(of_blocks[1].w), __float_as_int(of_blocks[2].w), __float_as_int(of_blocks[3].w));
@@ -982,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           // (little between a buffer's release and its copy: this code comes from a cold instruction cache)
           if (keys) {
             const int ks = k % S::kKStages;
-            ok = wait_warp(k_empty(ks), ((k / S::kKStages) & 1) ^ 1, abort_flag, 57);
+            ok = wait_warp(k_empty(ks), ((k / S::kKStages) & 1) ^ 1, limit, 57);
             if (!ok) break;
             if (!kTwoCopiers) publish();
             if (lane == 0) mbar_arrive_tx(k_full(ks), __popc(there) * kBlock * D);
@@ -999,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           if (values) {
             for (int h = 0; h < 2; ++h) {
               const int p = 2 * k + h, s = p % S::kSlots;
-              ok = wait_warp(raw_empty(s), ((p / S::kSlots) & 1) ^ 1, abort_flag, 58);
+              ok = wait_warp(raw_empty(s), ((p / S::kSlots) & 1) ^ 1, limit, 58);
               if (!ok) break;
               if (lane == 0) mbar_arrive_tx(raw_full(s), __popc(there >> (4 * h) & 0xFu) * kBlock * D);
               __syncwarp();
@@ -1014,9 +1021,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           }
           s0 = s1;
         }
-        if (*abort_flag) {  // let the copies in flight land before the CTA ends
-          for (int i = max(issued_k - S::kKStages, 0); i < issued_k; ++i) wait_bar_quiet(k_full(i % S::kKStages), (i / S::kKStages) & 1);
-          for (int i = max(issued_v - S::kSlots, 0); i < issued_v; ++i) wait_bar_quiet(raw_full(i % S::kSlots), (i / S::kSlots) & 1);
+        if (s_abort) {  // let the copies in flight land before the CTA ends
+          for (int i = max(issued_k - S::kKStages, 0); i < issued_k; ++i) wait_bar_quiet(k_full(i % S::kKStages), (i / S::kKStages) & 1, g.waits.limit_ns);
+          for (int i = max(issued_v - S::kSlots, 0); i < issued_v; ++i) wait_bar_quiet(raw_full(i % S::kSlots), (i / S::kSlots) & 1, g.waits.limit_ns);
         }
       } else if (warp == kIssuer) {
         // ------------------------------------------------ products: the whole warp walks the list, one lane issues; an
@@ -1028,12 +1035,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
         // is kept short, and the waits of a group are polled together.
         auto wait = [&](int code, auto... polls) {  // every lane polls for itself; the one that issues has seen the phases
           bool ok = true;
-          for (uint32_t n = 0; ok && !(polls() & ...); ++n) {
-            if ((n & 255) == 255 && (*abort_flag || n > kTries)) {
-              if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) atomicCAS(&g_chunk_error, 0, code);
+          for (uint32_t left = limit.tries; ok && !(polls() & ...); --left)
+            if (left == 0) {
+              limit.give_up(code);
               ok = false;
             }
-          }
           // No lane goes on before all have seen the phases: they turn every tile, and a lane that fell two turns behind
           // the one that issues would wait for a phase that is over.
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1182,7 +1188,7 @@ cudaError_t launch_t(const ChunkArgs& g, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv_chunk(const KvCache& c, const KvBatch& b, const KvAttention& a, int few, int dtype, cudaStream_t st) {
-  const ChunkArgs g{c, b, a, few, nullptr, nullptr};
+  const ChunkArgs g{c, b, a, waits(), few, nullptr, nullptr};
   return dtype == kBF16 ? launch_t<__nv_bfloat16>(g, st) : launch_t<__half>(g, st);
 }
 

@@ -92,9 +92,9 @@ __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, vol
 
 // Waits up to the limit for a phase without raising any flag (used to let the
 // copies still in flight land before a CTA exits).
-__device__ __forceinline__ void wait_bar_quiet(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void wait_bar_quiet(uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
   const uint64_t t0 = gtimer();
-  while (!mbar_try(bar, parity) && gtimer() - t0 < kWaitLimitNs) {
+  while (!mbar_try(bar, parity) && gtimer() - t0 < limit_ns) {
   }
 }
 

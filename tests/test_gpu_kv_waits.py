@@ -114,3 +114,31 @@ def test_per_thread_default_stream(nv):  # noqa: F811
     torch.cuda.synchronize()
     assert not any(status)
     assert all(torch.equal(o, w) for out, w in zip(outs, want) for o in out)
+
+
+STREAM_CODES, CHUNK_CODES = {41, 42, 43}, set(range(51, 67))
+
+
+@pytest.mark.parametrize("dim,dt", [(64, "f16"), (128, "bf16"), (128, "f16"), (256, "bf16"), (256, "f16")])
+@pytest.mark.parametrize("new,ctx", [(1, 30000), (300, 3000)])
+def test_a_wait_that_runs_out(nv, opt, new, ctx, dim, dt):  # noqa: F811
+    """Every second CTA waits for one arrival too many, so that waits run out after the shortened limit: the call comes back, an error code
+    says so, and after that was read the next call is right."""
+    s = Step(nv, 47, [new], [ctx], 4, 2, dim, 64, dt)
+    q, args, kw = s.rows(4).cuda(), (s.i32(s.table), s.i32(s.lengths)), dict(q_offsets=s.i32(s.offsets), max_q=new)
+    want = nv.kv_attention(q, s.kv, *args, **kw)
+    torch.cuda.synchronize()
+    assert nv.take_device_error() == 0
+    opt("wait_limit_us", 1000)
+    opt("test_withhold", 1)
+    start = time.perf_counter()
+    nv.kv_attention(q, s.kv, *args, **kw)
+    torch.cuda.synchronize()
+    elapsed = time.perf_counter() - start
+    opt("test_withhold", 0)
+    opt("wait_limit_us", 0)
+    code = nv.take_device_error()
+    assert code in (STREAM_CODES if new == 1 else CHUNK_CODES), code
+    assert 0.001 <= elapsed < 1.0
+    assert torch.equal(nv.kv_attention(q, s.kv, *args, **kw), want)
+    assert nv.take_device_error() == 0
