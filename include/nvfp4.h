@@ -424,7 +424,9 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const nvfp4_kv_batch* 
  * are captured into a graph have their own, one for each stream of a capture;
  * once every graph made from it is destroyed, a later capture may use it.
  * Graphs of different captures may run at the same time, two instances of one
- * capture's graph may not.
+ * capture's graph may not. A call whose bounded waits gave up (see
+ * nvfp4_take_device_error) gives no numbers for the rows that it could not
+ * finish, and leaves nothing behind for later calls.
  */
 nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_batch* batch, nvfp4_dtype dtype, const void* q,
                                 int64_t q_stride, int64_t heads, int64_t max_q, float scale, int64_t window, void* out,

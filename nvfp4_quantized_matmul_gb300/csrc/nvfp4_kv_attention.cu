@@ -685,7 +685,8 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
 
     bool fresh = true;           // the tile in work is the first one here of its head
     bool whole = out.tile == 0;  // this run holds the head from its first tile on
-    for (int it = 0; it < count; ++it) {
+    int it = 0;
+    for (; it < count; ++it) {
       if (fresh) begin();
       fresh = false;
       const int tok0 = (out.w.t0 + out.tile) * kTile, k_e = ek, v_e = ev;
@@ -728,6 +729,28 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
         in.next(g);
         find_page();
       }
+    }
+    // A wait gave up: the rest of the run comes out as no numbers, and its pieces are there for the joins, so that the
+    // counts are zero again after the call.
+    const float none = __int_as_float(0x7FC00000);
+    if (it < count && lane == 0) s_abort[warp] = 0;  // (a join's wait has a limit of its own)
+    while (it < count) {
+      const bool end = out.tile + 1 == out.w.nt;
+      if (end && whole) {
+        for (int j = lane; j < ROWS * D; j += 32) {
+          const int row = out.rt * ROWS + j / D, i = row / group;
+          if (i < out.w.sq.n)
+            static_cast<T*>(g.a.out)[(int64_t)(out.w.sq.first + i) * g.a.out_stride + (int64_t)(out.head * group + row % group) * D + j % D] = from_f32<T>(none);
+        }
+      } else if (end || it + 1 == count) {
+        const int piece = 2 * warp + (end ? 0 : 1);
+        const long long from = s_run[warp] + it - out.tile;
+        if (lane < ROWS) s_max[piece][lane] = s_max_e[piece][lane] = 0.f, s_sum[piece][lane] = none;
+        if (lane == 0)
+          s_piece[piece] = Piece{end ? warp_part(warp) : reinterpret_cast<float*>(stage), from, from + out.w.nt, out.rt, out.head, out.w.sq.first, out.w.sq.n};
+      }
+      if (end) whole = true;
+      if (++it < count) out.next(g);
     }
   }
   __syncthreads();
@@ -918,11 +941,11 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
               *reinterpret_cast<const float4*>(smem + at + i * kBytes + (d * ROWS + r) * 4));
       }
     }
-    if (!ok) return;
+    const float lost = ok ? 0.f : __int_as_float(0x7FC00000);
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int idx = tid + u * S::kThreads, d = idx % D, r = idx / D * 4;
-      const float4 xs[1] = {x[u]};
+      const float4 xs[1] = {make_float4(x[u].x + lost, x[u].y + lost, x[u].z + lost, x[u].w + lost)};
       if (idx < kItems) finish(pc, r, d, xs, s_inv[0]);
     }
     if (tid == 0) g.done[c0] = 0;
@@ -1094,22 +1117,6 @@ int read_kv_error() {
   if (v) {
     const int zero = 0;
     cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(int));
-    // a kernel that gave up may have left arrival counts behind
-    std::lock_guard<std::mutex> lock(g_ws_mu);
-    int cur = 0;
-    cudaGetDevice(&cur);
-    auto clear = [](const WorkspaceRef& w) {
-      if (!w) return;
-      cudaSetDevice(w->dev);
-      cudaDeviceSynchronize();
-      cudaMemset(w->p, 0, kDoneBytes);
-      cudaDeviceSynchronize();
-    };
-    for (auto& kv : g_ws)
-      if (!std::get<1>(kv.first)) clear(kv.second);
-    for (auto& w : g_ws_retired) clear(w);
-    for (auto& w : g_ws_captured) clear(w);
-    cudaSetDevice(cur);
   }
   return v;
 }

@@ -319,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
   __shared__ float4 s_scale[kMeta][8];  // of a tile's blocks: key scale, value exponent, 2^-value exponent, tokens (integer)
   __shared__ int s_tokens[kMeta];                                 // of a tile
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort, s_last, s_failed;
+  __shared__ int s_arrived[2];  // of the partial results: 0 not there yet, 1 counted, 2 counted as the last one
   // threads that share a row: the largest magnitude of its queries, and what each half has found
   // (its exponent)
   __shared__ uint8_t s_most[NQ == 1 ? ROWS : 1];
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
       mbar_init(meta_full(s), 1);
     }
     mbar_init(joined, 8);
-    s_abort = 0;
+    s_abort = s_failed = s_arrived[0] = s_arrived[1] = 0;
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (warp == 15) {
@@ -625,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
         // score and value exponent that the row's weights refer to (their sum, in m alone, up to kFar), denominator
         float m = -INFINITY, me = 0.f, l = 0.f;
         uint32_t piece_ph = 1;
+        bool finished = false;
         for (bool first = true;; first = false) {
           const bool more_pieces = w.left > 0;
           piece_ph ^= 1;
@@ -681,7 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
               const int c0 = cta_of(from), n = cta_of(to - 1) - c0 + 1;
               __threadfence();
               if (!meet()) break;
-              if (tid == 0) s_last = atomicAdd(g.done + c0, 1u) == (unsigned)(n - 1);
+              if (tid == 0) {
+                s_last = atomicAdd(g.done + c0, 1u) == (unsigned)(n - 1);
+                s_arrived[old.begins] = s_last ? 2 : 1;
+              }
               if (!meet()) break;
               if (s_last) {
                 __threadfence();
@@ -725,7 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
               if (!meet()) break;
             }
           }
-          if (!more_pieces) break;
+          if (!more_pieces) {
+            finished = true;
+            break;
+          }
           if (kHalves) {
             if (!wait_warp(q_full(q), piece_ph, limit, 52)) break;
             row.most = (uint32_t)s_most[r] << 23;
@@ -867,6 +875,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const ChunkArgs g
           if (!ok) break;
           old = Result{row.is, t_begin == w.it.t0, w.it.t1 - t_end, w.it.t1 - w.it.t0, at1 - (w.left - (t_end - t_begin)), row.out};
           w.advance(g, t_end);
+        }
+        // A wait gave up: the run's rows come out as no numbers, and what other CTAs count on still arrives, so that the
+        // counts are zero again after the call. (All softmax warps get here, since every wait ends.)
+        auto all_here = []() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        if (!finished) s_failed = 1;
+        all_here();
+        if (s_failed) {
+          for (Walk<ROWS> v = s_walk; v.left > 0;) {
+            const int end = v.piece_end();
+            const bool begins = v.t == v.it.t0;
+            bool lost = begins && end == v.it.t1;
+            if (!lost) {
+              const long long to = at1 - (v.left - (end - v.t)) + (v.it.t1 - end), from = to - (v.it.t1 - v.it.t0), longer = more * (each + 1);
+              auto cta_of = [&](long long at) { return (int)(at < longer ? at / (each + 1) : more + (at - longer) / each); };
+              const int c0 = cta_of(from), n = cta_of(to - 1) - c0 + 1;
+              if (s_arrived[begins] == 0) {
+                float* const part = g.ws + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * S::kPart;
+                for (int j = tid; j < ROWS; j += 256) part[(int64_t)ROWS * D + ROWS + j] = __int_as_float(0x7FC00000);
+                __threadfence();
+                all_here();
+                if (tid == 0) s_arrived[begins] = atomicAdd(g.done + c0, 1u) == (unsigned)(n - 1) ? 2 : 1;
+                all_here();
+              }
+              lost = s_arrived[begins] == 2;
+              if (lost && tid == 0) g.done[c0] = 0;
+            }
+            if (lost) {
+              for (int j = tid; j < ROWS * D / 2; j += 256) {
+                const int index = v.it.qt * ROWS + j / (D / 2), i = index / group;
+                if (i >= v.it.sq.n) break;
+                T* const y = static_cast<T*>(g.a.out) + (int64_t)(v.it.sq.first + i) * g.a.out_stride + (int64_t)(v.it.head * group + index % group) * D;
+                reinterpret_cast<uint32_t*>(y)[j % (D / 2)] = 0x7FFF7FFFu;  // two numbers that are none, in f16 and in bf16
+              }
+            }
+            v.advance(g, end);
+          }
         }
       }
     } else {

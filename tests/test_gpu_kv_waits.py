@@ -142,3 +142,27 @@ def test_a_wait_that_runs_out(nv, opt, new, ctx, dim, dt):  # noqa: F811
     assert 0.001 <= elapsed < 1.0
     assert torch.equal(nv.kv_attention(q, s.kv, *args, **kw), want)
     assert nv.take_device_error() == 0
+
+
+@pytest.mark.parametrize("dim,dt", [(64, "f16"), (128, "bf16"), (256, "bf16"), (256, "f16")])
+@pytest.mark.parametrize("new,ctx", [([1], [30000]), ([1] * 40, [211 * j % 4001 for j in range(40)]), ([300], [3000]),
+                                     ([200, 150, 40, 1], [100, 1900, 2000, 9000])], ids=lambda v: str(v)[:16])
+def test_calls_after_one_that_gave_up(nv, opt, new, ctx, dim, dt):  # noqa: F811
+    """What a call that gave up could not finish is no number and the rest is right, and the calls after it on the stream are
+    right although nobody has asked for the error: nothing of it is left behind."""
+    s = Step(nv, 48, new, ctx, 4, 2, dim, 64, dt)
+    q, args, kw = s.rows(4).cuda(), (s.i32(s.table), s.i32(s.lengths)), dict(q_offsets=s.i32(s.offsets), max_q=max(new))
+    want = nv.kv_attention(q, s.kv, *args, **kw)
+    out = torch.zeros_like(want)
+    for _ in range(2):
+        opt("wait_limit_us", 1000)
+        opt("test_withhold", 1)
+        nv.kv_attention(q, s.kv, *args, out=out, **kw)
+        opt("test_withhold", 0)
+        opt("wait_limit_us", 0)
+        lost = torch.isnan(out).all(-1)
+        assert lost.any() and torch.equal(out[~lost], want[~lost])
+        for _ in range(3):
+            assert torch.equal(nv.kv_attention(q, s.kv, *args, **kw), want)
+    assert nv.take_device_error() in STREAM_CODES | CHUNK_CODES
+    assert nv.take_device_error() == 0
