@@ -21,7 +21,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
 SOURCES = ["nvfp4_api.cu", "nvfp4_stream.cu", "nvfp4_qmv.cu", "nvfp4_qmv_tma.cu", "nvfp4_qmv_stream.cu", "nvfp4_qmm_tc.cu",
-           "nvfp4_qmv_nt.cu", "nvfp4_kv_append.cu", "nvfp4_kv_attention.cu", "nvfp4_kv_chunk.cu"]
+           "nvfp4_qmv_nt.cu", "nvfp4_kv_append.cu", "nvfp4_kv_attention.cu", "nvfp4_kv_chunk.cu",
+           "nvfp4_kv_workspace.cu"]
 
 
 def _nvcc() -> str:

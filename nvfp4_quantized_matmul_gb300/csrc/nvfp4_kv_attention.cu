@@ -48,11 +48,6 @@
 // pair a lane, and its weights are already the second product's operand,
 // whose value operand is then one 16-byte load (a channel's 16 tokens).
 #include <atomic>
-#include <map>
-#include <memory>
-#include <mutex>
-#include <tuple>
-#include <vector>
 
 #include "nvfp4_kv.cuh"
 #include "nvfp4_pipe.cuh"
@@ -953,76 +948,7 @@ __global__ void __launch_bounds__(Shape<T, D, ROWS>::kThreads, 1) kv_stream_kern
   }
 }
 
-// Partial results and arrival counts: two calls that may run at the same time never share them. A stream's calls have one
-// allocation, made on the first call that needs it, grown on demand and kept until release_kv_workspaces(). Calls captured
-// into a graph run wherever the graph is launched, so each capture has its own, which its graph keeps hold of; when the last
-// graph made from the capture is gone, the next capture may have it. The counts are zero between calls.
-struct Workspace {
-  char* p = nullptr;
-  size_t bytes = 0;
-  int dev = 0;
-  std::atomic<bool> idle{false};  // of a capture whose graphs are gone
-};
-using WorkspaceRef = std::shared_ptr<Workspace>;
-// device, capture (0: none), stream: the handle, or a number of the calling thread's own
-using WorkspaceKey = std::tuple<int, unsigned long long, unsigned long long>;
-std::mutex g_ws_mu;
-std::map<WorkspaceKey, WorkspaceRef> g_ws;
-std::vector<WorkspaceRef> g_ws_retired;   // outgrown ones, which queued calls may still use
-std::vector<WorkspaceRef> g_ws_captured;  // all that captures have or had
-
-// Called when nothing holds a captured graph any more, on a thread of the driver's: no CUDA calls, no locks.
-void CUDART_CB release_captured(void* ref) {
-  const std::unique_ptr<WorkspaceRef> p(static_cast<WorkspaceRef*>(ref));
-  (*p)->idle.store(true, std::memory_order_release);
-}
-
-// A cleared allocation. Cleared here and now, not by the stream: while that is captured, its graph would do it.
-cudaError_t make_workspace(int dev, size_t bytes, size_t clear, WorkspaceRef* out) {
-  char* p = nullptr;
-  cudaStream_t own = nullptr;
-  cudaError_t e = cudaMalloc(&p, bytes);
-  if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
-  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, clear, own);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(own);
-  if (own) cudaStreamDestroy(own);
-  if (e != cudaSuccess) {
-    cudaFree(p);
-    return e;
-  }
-  *out = std::make_shared<Workspace>();
-  (*out)->p = p;
-  (*out)->bytes = bytes;
-  (*out)->dev = dev;
-  return cudaSuccess;
-}
-
-// For a capture: one whose graphs are gone, or a new one; `graph` then holds it.
-cudaError_t captured_workspace(int dev, size_t bytes, size_t clear, cudaGraph_t graph, WorkspaceRef* out) {
-  for (auto it = g_ws.begin(); it != g_ws.end();)
-    it = std::get<1>(it->first) && it->second && it->second->idle ? g_ws.erase(it) : std::next(it);
-  for (const WorkspaceRef& w : g_ws_captured)
-    if (w->dev == dev && w->bytes >= bytes && w->idle.exchange(false, std::memory_order_acquire)) {
-      *out = w;
-      break;
-    }
-  cudaError_t e;
-  if (!*out) {
-    if ((e = make_workspace(dev, bytes, clear, out)) != cudaSuccess) return e;
-    g_ws_captured.push_back(*out);
-  }
-  WorkspaceRef* ref = new WorkspaceRef(*out);
-  cudaUserObject_t holder;
-  if ((e = cudaUserObjectCreate(&holder, ref, release_captured, 1, cudaUserObjectNoDestructorSync)) != cudaSuccess) {
-    release_captured(ref);
-    return e;
-  }
-  if ((e = cudaGraphRetainUserObject(graph, holder, 1, cudaGraphUserObjectMove)) != cudaSuccess) cudaUserObjectRelease(holder, 1);
-  return e;
-}
-
 constexpr int kDevices = 64;
-constexpr size_t kDoneBytes = 4 * kKvMaxCtas;
 
 template <typename T, int D, int ROWS>
 cudaError_t launch_shape(AttnArgs g, cudaStream_t st) {
@@ -1061,37 +987,6 @@ cudaError_t launch_t(const AttnArgs& g, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t kv_workspace(int dev, cudaStream_t st, size_t bytes, unsigned** done, float** parts) {
-  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-  unsigned long long capture = 0, stream = reinterpret_cast<uintptr_t>(st);
-  cudaGraph_t graph = nullptr;
-  cudaError_t e;
-  if (st != nullptr && st != cudaStreamLegacy) {  // which cannot be captured, and may not be asked during other captures
-    if ((e = cudaStreamGetCaptureInfo(st, &status, &capture, &graph)) != cudaSuccess) return e;
-    if (status != cudaStreamCaptureStatusActive) capture = 0;
-    if (st == cudaStreamPerThread) {  // one handle, a stream of each thread
-      if ((e = cudaStreamGetId(st, &stream)) != cudaSuccess) return e;
-      stream |= 1ull << 63;
-    }
-  }
-  bytes += kDoneBytes;
-  std::lock_guard<std::mutex> lock(g_ws_mu);
-  WorkspaceRef& w = g_ws[WorkspaceKey{dev, capture, stream}];
-  if (!w || w->bytes < bytes) {
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
-    WorkspaceRef made;
-    e = capture ? captured_workspace(dev, bytes, kDoneBytes, graph, &made) : make_workspace(dev, bytes, kDoneBytes, &made);
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess) return e;
-    if (w && !capture) g_ws_retired.push_back(w);
-    w = made;
-  }
-  *done = reinterpret_cast<unsigned*>(w->p);
-  *parts = reinterpret_cast<float*>(w->p + kDoneBytes);
-  return cudaSuccess;
-}
-
 cudaError_t launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAttention& a, int dtype, cudaStream_t st) {
   // one sequence has all the tokens; of several, max_q bounds each
   const int64_t most = b.seqs == 1 || a.max_q > b.tokens ? b.tokens : a.max_q;
@@ -1119,17 +1014,6 @@ int read_kv_error() {
     cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(int));
   }
   return v;
-}
-
-void release_kv_workspaces() {
-  std::lock_guard<std::mutex> lock(g_ws_mu);
-  for (auto& kv : g_ws)
-    if (kv.second && !std::get<1>(kv.first)) cudaFree(kv.second->p);
-  for (auto& w : g_ws_retired) cudaFree(w->p);
-  for (auto& w : g_ws_captured) cudaFree(w->p);  // (what graphs still hold is the description alone)
-  g_ws.clear();
-  g_ws_retired.clear();
-  g_ws_captured.clear();
 }
 
 }  // namespace nvfp4
