@@ -999,7 +999,8 @@ cudaError_t launch_kv_attention(const KvCache& c, const KvBatch& b, const KvAtte
     const cudaError_t e = launch_kv_chunk(c, b, a, all ? 0 : few, dtype, st);
     if (e != cudaSuccess || all) return e;
   }
-  const AttnArgs g{c, b, a, waits(), chunks ? few : 0x7FFFFFFF, nullptr, nullptr};
+  AttnArgs g{c, b, a, waits(), chunks ? few : 0x7FFFFFFF, nullptr, nullptr};
+  g.a.max_q = most;  // (the caller's may be any number; times the group it would overflow)
   return dtype == kBF16 ? launch_t<__nv_bfloat16>(g, st) : launch_t<__half>(g, st);
 }
 

@@ -187,3 +187,13 @@ def test_more_new_tokens_than_the_length(nv, new, ctx, heads, kv_heads, dim, win
     for b, c in enumerate(ctx):
         if c < 0:
             assert (y[int(s.offsets[b]):int(s.offsets[b]) - c] == 0).all()
+
+
+@pytest.mark.parametrize("new,ctx", [([3], [500]), ([1, 3], [70, 30]), ([60], [3])])
+def test_any_large_bound_on_the_new_tokens(nv, new, ctx):  # noqa: F811
+    """max_q beyond the tokens there are is no different from their number, whatever it is."""
+    s = Step(nv, 58, new, ctx, 8, 2, 128, 32, "bf16")
+    q, args, off = s.rows(8).cuda(), (s.i32(s.table), s.i32(s.lengths)), s.i32(s.offsets)
+    want = nv.kv_attention(q, s.kv, *args, q_offsets=off, max_q=sum(new))
+    for max_q in (2**31, 2**61, 2**62, 2**63 - 1):
+        assert torch.equal(nv.kv_attention(q, s.kv, *args, q_offsets=off, max_q=max_q), want)
