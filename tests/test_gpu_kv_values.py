@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import kv_oracle as K
-from test_gpu_kv import DT, HALF_ULP, Step, nv  # noqa: F401
+from test_gpu_kv import DT, HALF_ULP, Step, check_append, nv, tables  # noqa: F401
 
 # (the oracle's own bound on the results, which grows with the scores, overflows here and is not used)
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:overflow encountered", "ignore:invalid value encountered")]
@@ -197,3 +197,72 @@ def test_any_large_bound_on_the_new_tokens(nv, new, ctx):  # noqa: F811
     want = nv.kv_attention(q, s.kv, *args, q_offsets=off, max_q=sum(new))
     for max_q in (2**31, 2**61, 2**62, 2**63 - 1):
         assert torch.equal(nv.kv_attention(q, s.kv, *args, q_offsets=off, max_q=max_q), want)
+
+
+def check_sharp(s, q, scale=None):
+    """`Step.check`, where zeros, or a mean of the values without any scores, would not pass."""
+    scale = s.dim**-0.5 if scale is None else scale
+    y, ref, bound = s.attend(q, scale)
+    mean, _ = K.attention(np.zeros(q.shape), s.cache, s.table, s.lengths, s.offsets, scale)
+    lim = bound + HALF_ULP[s.dt] * np.abs(ref) + 2.0**-24
+    several = np.repeat([int(n) - int(m) > 1 for n, m in zip(s.lengths, s.new)], s.new)  # rows that see one key have no choice
+    assert (np.abs(ref) > lim)[several].mean() > 0.9 and (np.abs(ref - mean) > lim)[several].mean() > 0.9
+    err = np.abs(y.double().cpu().numpy() - ref)
+    assert (err <= lim).all(), float((err / lim).max())
+
+
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("size", ["large", "one", "small"])
+def test_query_sizes_that_count(nv, dim, dt, new, size):  # noqa: F811
+    """Scores near one from queries of any size: the error that is let through is a few percent of the results."""
+    up = {"large": 1e4 if dt == "f16" else 1e30, "one": 1.0, "small": 2.0**-10 if dt == "f16" else 1e-30}[size]
+    s = Step(nv, 59, [new], [200], 4, 2, dim, 32, dt)
+    q = s.rows(4).float()
+    check_sharp(s, (q * up).to(DT[dt]), scale=float(np.float32(dim**-0.5 / up)))
+
+
+# A block of threads has 160 to 512 of them: beyond, a thread looks after several sequences.
+@pytest.mark.parametrize("seqs", [193, 353, 513, 1100])
+@pytest.mark.parametrize("heads,kv_heads,dim,dt", [(2, 1, 64, "bf16"), (12, 1, 64, "f16"), (4, 2, 128, "bf16"), (12, 1, 128, "f16"),
+                                                   (2, 1, 256, "bf16"), (4, 2, 256, "f16")])
+def test_single_tokens_of_many_sequences(nv, seqs, heads, kv_heads, dim, dt):  # noqa: F811
+    ctx = np.random.default_rng(seqs).integers(0, 50, size=seqs)
+    ctx[::7] = 0
+    ctx[5] = 500
+    s = Step(nv, 60, [1] * seqs, list(ctx), heads, kv_heads, dim, 16, dt)
+    check_sharp(s, s.rows(heads))
+
+
+@pytest.mark.parametrize("seqs", [511, 513, 1100])
+@pytest.mark.parametrize("heads,kv_heads,dim,dt,new", [(12, 1, 64, "bf16", 9), (8, 1, 128, "bf16", 5), (4, 1, 256, "f16", 3)])
+def test_runs_of_many_sequences(nv, seqs, heads, kv_heads, dim, dt, new):  # noqa: F811
+    """Sequences of the tensor-core kernel with single tokens and idle sequences between them."""
+    g = np.random.default_rng(seqs + 1)
+    n = np.where(g.random(seqs) < 0.15, new, g.integers(0, 2, size=seqs))
+    n[[0, seqs - 1]] = new
+    s = Step(nv, 61, list(n), list(g.integers(0, 30, size=seqs)), heads, kv_heads, dim, 16, dt)
+    check_sharp(s, s.rows(heads))
+
+
+@pytest.mark.parametrize("seqs", [33, 513, 1100])
+def test_append_of_many_sequences(nv, seqs):  # noqa: F811
+    """Single tokens, idle sequences and a chunk in one call."""
+    g = np.random.default_rng(seqs + 2)
+    n = g.integers(0, 2, size=seqs)
+    n[seqs // 2] = 70
+    s = Step(nv, 62, list(n), list(g.integers(0, 60, size=seqs)), heads=2, kv_heads=1, dim=64, page=16)
+    check_append(s, s.rows(1), s.rows(1), s.rows(2), *tables(256, 64), q_offsets=s.i32(s.offsets))
+
+
+@pytest.mark.parametrize("dim,dt", SIZES)
+@pytest.mark.parametrize("new", [[1, 1, 1], [2, 1, 60], [130]])
+def test_queries_that_are_no_numbers(nv, dim, dt, new):  # noqa: F811
+    """A query with an infinity or no number gives no numbers, the other queries and heads what they give without it."""
+    s = Step(nv, 63, new, [70] * len(new), 4, 2, dim, 32, dt)
+    q = s.rows(4)
+    want = s.check(q)
+    q[0, 1, 3], q[0, 2, dim - 1], q[sum(new) - 1, 0, 0] = float("nan"), float("inf"), float("-inf")
+    y = nv.kv_attention(q.cuda(), s.kv, s.i32(s.table), s.i32(s.lengths), q_offsets=s.qo(), max_q=max(new))
+    bad = ~torch.isfinite(q).all(-1)
+    assert torch.isnan(y[bad.cuda()]).all() and torch.equal(y[~bad.cuda()], want[~bad.cuda()])
