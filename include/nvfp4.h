@@ -417,8 +417,13 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const nvfp4_kv_batch* 
  *   q, out [tokens, heads, head_dim] of dtype, *_stride elements between
  *   tokens, aligned as for nvfp4_kv_append; max_q: a bound on the new tokens
  *   of any one sequence, which chooses between kernels.
- * Products and sums are taken in f32, the softmax's weights rounded to f16
- * before the second product. Scratch: partial results of up to two parts of a
+ * Products and sums are taken in f32. Queries are used as they are down to
+ * 2^-13 of a row's largest, below that to within 2^-21 (bf16) or 2^-24 (f16)
+ * of it. The softmax's weights are rounded to f16 before the second product:
+ * 2^-12 of each, or 2^-32 of the largest where that is more, largest by weight
+ * times the value scale of the key's block. Scores, scale * q . k, may be of
+ * any size in f32 (up to 2^126); a row with larger ones gives no numbers.
+ * Scratch: partial results of up to two parts of a
  * head per SM and one per warp (5 to 41 MB on 152 SMs), per (device, stream),
  * the per-thread default stream counting as one for each thread. Calls that
  * are captured into a graph have their own, one for each stream of a capture;

@@ -26,8 +26,9 @@ namespace kv {
 
 constexpr int kBlock = 16;  // tokens that share a scale
 // Range of the scales' exponents. The attention weighs a key by 2^(score +
-// value exponent) in f32, so the exponents' span (96) plus the 24 binades in
-// which a score still counts stays within f32's normal range.
+// value exponent) against the heaviest one's in f32, so the exponents' span
+// (96) plus the 24 binades in which a score still counts stays within f32's
+// normal range.
 constexpr int kExpMin = -48, kExpMax = 48;
 
 // Byte of (token r, channel d) in a key block of D channels.
@@ -106,7 +107,9 @@ inline Waits waits() {
 }
 
 // New tokens and tokens in all of sequence b, made safe against offsets that
-// do not fit: first .. first + n lie within [0, tokens], n <= length.
+// do not fit: first .. first + n lie within [0, tokens], length within what
+// the table holds. There may be more new tokens than the length says: the
+// first ones' positions are negative then.
 struct Seq {
   int first, n, length;
 };

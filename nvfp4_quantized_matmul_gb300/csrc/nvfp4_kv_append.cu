@@ -14,7 +14,9 @@
 // Bound by bytes: 16384 tokens of 32 query and 16 key/value heads of 128
 // bf16 channels move 478 MB in 95 us, 5.0 TB/s, 74% of a plain copy's rate
 // (a CTA's load latency, with 28 warps an SM to cover it, takes the rest). A
-// single token takes 3.3 us, most of them the launch.
+// single token takes 3.3 us, most of them the launch. Times here are those of
+// captured graphs; a call from the Python binding takes 20 us at least, its
+// host side.
 #include "nvfp4_kv.cuh"
 
 namespace nvfp4 {

@@ -16,8 +16,9 @@
 // Bound by the cache's bytes: an SM receives about 23 bytes a cycle at the
 // measured copy rate. One token of 64 sequences (1 to 8191 keys, 32 / 16
 // heads of 128) takes 195 us, 5.8 TB/s, 86% of a copy's rate; one token over
-// 131072 keys (32 / 4 heads) 37 us, of which 20 are the bytes; one token over
-// 500 keys 9.7 us.
+// 131072 keys (32 / 4 heads) 38 us, of which 20 are the bytes; one token over
+// 500 keys 10.1 us. Times here are those of captured graphs; a call from the
+// Python binding takes 14 us at least, its host side.
 //
 // The work is the list of 64-token tiles of every (sequence, row tile,
 // key/value head), from lengths read on the device, in equal contiguous
@@ -38,9 +39,11 @@
 // smallest step. Up to eight rows, the first two terms are the upper and lower
 // half of one 16-row operand. The weights p are rounded to f16 (scaled by
 // 2^14, so that a key counts until it is 2^38 lighter than the heaviest) and
-// multiply values converted to f16, which is exact; the values are the
-// 16-row operand (sixteen channels) and up to eight rows of weights the
-// other, so that no half of it is wasted on few rows.
+// multiply values converted to f16, which is exact: half the tensor time of a
+// product in f32's 10-bit form, and a key lighter than 2^-28 of the heaviest,
+// whose weight has fewer than 11 bits, is off by 2^-39 of that at most. The
+// values are the 16-row operand (sixteen channels) and up to eight rows of
+// weights the other, so that no half of it is wasted on few rows.
 //
 // Fragments: lane (g, t) = (lane / 4, lane % 4). Score column c of step j
 // (j = 0..7) is token 16 (c / 2) + 2 j + c % 2 of the tile, so that lane
@@ -66,15 +69,24 @@ constexpr int kTile = 64;      // tokens a tile
 constexpr int kMinShare = 4;
 // Heads of up to so many tiles stay in one CTA: half of them more or less in a share is worth less time than joining
 // between CTAs. 32 sequences of 5 tokens and 16 heads, 16 tiles each: 48.5 us, 57.0 without; 300 short sequences: 23.6
-// and 27.7; 64 long ones, where it moves no end worth mentioning, the same.
+// and 27.7; 64 long ones, where it moves no end worth mentioning, the same. One token of 16 heads of 128, with and without:
+//                 400 keys     1024         1536         1600 (25 tiles: no head is kept whole)
+//   1 sequence    10.1, 14.2   14.4, 13.4   16.8, 13.5   13.6
+//   4             10.2, 15.6   14.4, 16.6   17.0, 16.1   18.4
+//   10            12.9, 17.0   21.0, 24.2   26.1, 28.1   28.7
+//   20            15.8, 21.7   28.1, 31.2   36.2, 37.4   37.7
+// so it costs up to a quarter where a few long heads are all there is, and gains elsewhere.
 constexpr int kWholeHead = 24;
 constexpr float kPUp = 14.0f;  // the weights are held times 2^14
 // A sequence of more query rows (new tokens x heads of a group) goes to the
 // tensor-core kernel of nvfp4_kv_chunk.cu. This one's time grows with every 16
 // rows, that one's not up to 128. Here and there, 16 sequences:
-//    64 channels, group 12:  72 rows 28 us, 33 us    132 rows  38 us, 33 us
-//   128 channels, group 2:   32 rows 119 us, 137 us   48 rows 166 us, 135 us
-//   256 channels, group 2:    8 rows 67 us, 79 us     16 rows 122 us, 73 us
+//    64 channels, group 12:  72 rows 30 us, 32 us     132 rows  41 us, 32 us
+//   128 channels, group 2:   32 rows 127 us, 136 us    48 rows 177 us, 134 us
+//   256 channels, group 2:    8 rows 67 us, 77 us      16 rows  90 us, 72 us
+// 32 sequences, 128 channels, group 8: 32 rows 86 us, 105 us, 40 rows 124 us,
+// 107 us. (A single sequence is the exception: 14000 keys, group 8, 64 rows
+// take 46 us here and 53 there.)
 constexpr int few_rows(int64_t head_dim) { return head_dim == 64 ? 96 : head_dim == 128 ? 32 : 8; }
 
 struct AttnArgs {
@@ -973,8 +985,8 @@ cudaError_t launch_shape(AttnArgs g, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Sixteen rows a tile only where there may be more than eight: one token of 64 sequences takes 199 us with eight and 260
-// with sixteen, whose second half would be empty; of one sequence of 131072 keys 39 and 61.
+// Sixteen rows a tile only where there may be more than eight: one token of 64 sequences takes 193 us with eight and 266
+// with sixteen, whose second half would be empty; of one sequence of 131072 keys 38 and 58.
 template <typename T>
 cudaError_t launch_t(const AttnArgs& g, cudaStream_t st) {
   const bool few = (g.a.max_q * g.a.group < g.few ? g.a.max_q * g.a.group : g.few) <= 8;

@@ -12,13 +12,17 @@
 //               row's largest, and within 2^-21 (bf16) or 2^-24 (f16) of it
 //               below that: further terms in E4M3 would share the first
 //               one's smallest step of 2^-9 and end at 2^-17
-//   P = 2^(t - m) in f16, written over S
+//   P = 2^(t - m + 7) in f16, written over S: products with f32's 10-bit form
+//               would take twice the time. A key lighter than 2^-21 of the
+//               heaviest has fewer than 11 bits, none below 2^-32: that is
+//               what it is off by at most, 2^-15 in all of 2^17 such keys
 //   O += P V    kind::f16: P from TMEM, values converted to f16 (exactly)
 // Bound by the tensor cores where a chunk is long: 2048 tokens at 14000 keys
-// (32 / 16 heads of 128, bf16) take 351 us, 1434 TFLOP/s, 76% of the measured
-// bf16 rate; a prompt of 8192 (32 / 4 heads) 414 us, 70%; six prompts of 100
-// to 2500 tokens with 256 channels, f16, 188 us, 39% (three query terms, and
-// queries and results of a block of rows last as long as four tiles).
+// (32 / 16 heads of 128, bf16) take 353 us, 1427 TFLOP/s, 75% of the measured
+// bf16 rate; a prompt of 8192 (32 / 4 heads) 419 us, 69%; six prompts of 100
+// to 2500 tokens with 256 channels, f16, 196 us, 38% (three query terms, and
+// queries and results of a block of rows last as long as four tiles). Times
+// here are those of captured graphs.
 //
 // Roles: a warpgroup per 128 rows for the softmax (a thread is a row, so
 // maxima and sums need no exchange), four warps that convert values, one that
